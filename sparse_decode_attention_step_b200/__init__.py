@@ -1,6 +1,6 @@
 """Python binding of the SAGA + Atop-N decode attention library (sm_100a).
 
-A thin ctypes layer over ``include/saga.h``: the same entry points, the same
+A thin ctypes layer over ``include/saga.h`` (and ``saga_merge.h``, ``saga_q4.h``): the same entry points, the same
 argument order, and argument marshalling only (device pointers from torch
 tensors or plain integers, the CUDA stream handle). Every step of the
 computation runs in the CUDA library ``_lib/libsaga_b200.so``; there is no
@@ -50,10 +50,17 @@ class saga_merge_shape(ctypes.Structure):
                 ("h_k", ctypes.c_int32), ("d", ctypes.c_int32)]
 
 
+class saga_q4_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("k_g", ctypes.c_void_p), ("v_g", ctypes.c_void_p)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _SP = ctypes.POINTER(saga_shape)
 _MP = ctypes.POINTER(saga_merge_shape)
+_CP = ctypes.POINTER(saga_q4_cache)
 
 _SIGS = {
     "saga_shape_contiguous": (None, [_SP, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
@@ -78,6 +85,16 @@ _SIGS = {
     "saga_merge_workspace_size": (ctypes.c_size_t, [_MP]),
     "saga_merge_keys": (ctypes.c_int, [_MP, _P, _P, _P, ctypes.c_double, _P, _P, _P, _P, _P,
                                        ctypes.c_size_t, _P]),
+    "saga_q4_workspace_size": (ctypes.c_size_t, [_SP]),
+    "saga_q4_append_kv": (ctypes.c_int, [_SP, _CP, _P, _P, ctypes.c_int32, _P, _P, _P,
+                                         ctypes.c_size_t, _P]),
+    "saga_q4_read_kv": (ctypes.c_int, [_SP, _CP, _P, ctypes.c_int64, _P, _P, _P, _P,
+                                       ctypes.c_size_t, _P]),
+    "saga_q4_dense_decode": (ctypes.c_int, [_SP, _CP, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "saga_q4_decode_step": (ctypes.c_int, [_SP, _CP, _P, _P, _P, _P, _P, _P, _P,
+                                           ctypes.c_size_t, _P]),
+    "saga_q4_refresh_threshold": (ctypes.c_int, [_SP, _CP, _P, _P, ctypes.c_int32, _P, _P, _P, _P,
+                                                 _P, _P, ctypes.c_size_t, _P]),
 }
 
 
@@ -272,3 +289,96 @@ def merge_keys(mshape, X, W_K, Q, rcond, w, pairs, W_S, ws, total=None, stream=N
     _check(load().saga_merge_keys(ctypes.byref(mshape), _ptr(X), _ptr(W_K), _ptr(Q),
                                   float(rcond), _ptr(w), _ptr(pairs), _ptr(total), _ptr(W_S),
                                   p, n, _stream(stream)), "saga_merge_keys")
+
+
+# ---------------------------------------------------------------------------
+# the decode step over a KV cache held in 4 bits (include/saga_q4.h)
+# ---------------------------------------------------------------------------
+class Q4Cache:
+    """The 4-bit caches of one shape: codes [B][h][cap][d/2] and scales
+    [B][h][cap][d/16] (uint8) of K and V, and an optional fp32 scale per head
+    (k_g [h_k], v_g [h_v]). Arrays not given are allocated through torch, with
+    the shape's strides."""
+
+    def __init__(self, shp, k_codes=None, k_scales=None, v_codes=None, v_scales=None, k_g=None,
+                 v_g=None, device="cuda"):
+        def given(x, stride_b, stride_h, h, per):
+            if x is not None:
+                return x
+            import torch
+            buf = torch.zeros(shp.B * stride_b // per, dtype=torch.uint8, device=device)
+            return buf.as_strided((shp.B, h, shp.cap, shp.d // per),
+                                  (stride_b // per, stride_h // per, shp.d // per, 1))
+        self.k_codes = given(k_codes, shp.k_stride_b, shp.k_stride_h, shp.h_k, 2)
+        self.k_scales = given(k_scales, shp.k_stride_b, shp.k_stride_h, shp.h_k, 16)
+        self.v_codes = given(v_codes, shp.v_stride_b, shp.v_stride_h, shp.h_v, 2)
+        self.v_scales = given(v_scales, shp.v_stride_b, shp.v_stride_h, shp.h_v, 16)
+        self.k_g, self.v_g = k_g, v_g
+        self.c = saga_q4_cache(_ptr(self.k_codes), _ptr(self.k_scales), _ptr(self.v_codes),
+                               _ptr(self.v_scales), _ptr(k_g), _ptr(v_g))
+
+
+def q4_workspace_size(shp):
+    return int(load().saga_q4_workspace_size(ctypes.byref(shp)))
+
+
+class Q4Workspace:
+    """Device workspace for the q4 calls of one shape, allocated through torch;
+    its error word is zeroed."""
+
+    def __init__(self, shp, device="cuda", stream=None):
+        import torch
+        self.nbytes = q4_workspace_size(shp)
+        if self.nbytes == 0:
+            raise SagaError(SAGA_ERR_INVALID_ARG, "saga_q4_workspace_size")
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        workspace_init(self.buf, self.nbytes, stream)
+
+    def data_ptr(self):
+        return self.buf.data_ptr()
+
+
+def q4_append_kv(shp, cache, k_new, v_new, T, l_kv, ws, n_new=None, stream=None):
+    """Quantise T new rows per sequence (n_new[b] of them where given), k_new
+    [B][T][h_k][d] and v_new [B][T][h_v][d], write them at position l_kv[b]
+    and grow l_kv."""
+    p, n = _ws(ws)
+    _check(load().saga_q4_append_kv(ctypes.byref(shp), ctypes.byref(cache.c), _ptr(k_new),
+                                    _ptr(v_new), T, _ptr(n_new), _ptr(l_kv), p, n,
+                                    _stream(stream)), "saga_q4_append_kv")
+
+
+def q4_read_kv(shp, cache, n, l_kv, K, V, ws, start=None, stream=None):
+    """Rows start[b] .. start[b] + n - 1 of every head into K [B][h_k][n][d] and
+    V [B][h_v][n][d]; rows at or behind l_kv[b] are left as they were."""
+    p, nb = _ws(ws)
+    _check(load().saga_q4_read_kv(ctypes.byref(shp), ctypes.byref(cache.c), _ptr(start), n,
+                                  _ptr(l_kv), _ptr(K), _ptr(V), p, nb, _stream(stream)),
+           "saga_q4_read_kv")
+
+
+def q4_dense_decode(shp, cache, q, l_kv, out, ws, stream=None):
+    """Full attention over a 4-bit cache, with the shape's key and value head maps."""
+    p, n = _ws(ws)
+    _check(load().saga_q4_dense_decode(ctypes.byref(shp), ctypes.byref(cache.c), _ptr(q),
+                                       _ptr(l_kv), _ptr(out), p, n, _stream(stream)),
+           "saga_q4_dense_decode")
+
+
+def q4_decode_step(shp, cache, q, l_kv, tau, out, ws, sel_count=None, sel_mask=None, stream=None):
+    """One Atop-N step with stored thresholds over a 4-bit cache."""
+    p, n = _ws(ws)
+    _check(load().saga_q4_decode_step(ctypes.byref(shp), ctypes.byref(cache.c), _ptr(q),
+                                      _ptr(l_kv), _ptr(tau), _ptr(out), _ptr(sel_count),
+                                      _ptr(sel_mask), p, n, _stream(stream)),
+           "saga_q4_decode_step")
+
+
+def q4_refresh_threshold(shp, cache, q, l_kv, N, tau, ws, out=None, sel_count=None, sel_mask=None,
+                         scores=None, stream=None):
+    """Exact N-th largest scores over a 4-bit cache into tau; with out, the step too."""
+    p, n = _ws(ws)
+    _check(load().saga_q4_refresh_threshold(ctypes.byref(shp), ctypes.byref(cache.c), _ptr(q),
+                                            _ptr(l_kv), N, _ptr(tau), _ptr(out), _ptr(sel_count),
+                                            _ptr(sel_mask), _ptr(scores), p, n, _stream(stream)),
+           "saga_q4_refresh_threshold")

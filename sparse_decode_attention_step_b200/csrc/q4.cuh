@@ -1,0 +1,223 @@
+// What the 4-bit cache kernels share: the row format, its conversion to fp16
+// MMA operands, and the score tile.
+//
+// A row of D values is D/2 bytes of e2m1 codes and D/16 e4m3 scales. In fp16
+// both factors and their product are exact: a code has 2 significant bits, a
+// scale 4, and code * scale has at most 6 and lies between 2^-10 and 2688. The
+// scale byte moved to bits 7..14 of a half is the scale times 2^-8 (subnormal
+// scales become subnormal halves), so one integer multiply converts it, and
+// operands built this way carry a common factor 2^-8 that the kernels take out
+// in fp32. Any byte therefore reads as a finite value, stale ones included.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "sm100.cuh"
+
+namespace saga {
+
+// Strides of the code arrays in bytes; the scale arrays have an eighth of them
+// (D/2 code bytes to D/16 scale bytes a row).
+struct Q4Params {
+  const void *q;
+  const uint8_t *kc, *ks, *vc, *vs;
+  const float *k_g, *v_g;      // nullable [h_k], [h_v]
+  const int32_t *l_kv;
+  const float *tau;
+  float *partials;             // [B][h_q][S][d + kRecPad] (dense)
+  float *scores_out;           // dump: [B][h_q][row_stride]
+  uint8_t *sel_mask;           // nullable [B][h_q][row_stride]
+  uint32_t *hist;              // dump: [B][h_q][256] top-byte histograms
+  uint32_t *lmask;             // step: the kept lists, as in StepParams
+  float *lscore;
+  int64_t nblk;
+  int32_t *err, *abort;
+  int64_t q_sb, q_sh;          // elements
+  int64_t kc_sb, kc_sh, vc_sb, vc_sh;
+  int64_t cap, max_l_kv, row_stride, split_len;
+  int32_t B, h_q, h_k, h_v, S;
+  float scale;                 // 1 / sqrt(d)
+};
+
+constexpr float kQ4Unit = 256.f;   // what the fp16 operands are scaled down by
+
+namespace q4 {
+
+// Four bytes of codes: their eight values as four f16x2, in order.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+// A scale byte in both halves, times 2^-8.
+__device__ __forceinline__ uint32_t scale_f16(uint32_t byte) { return (byte & 0x7fu) * 0x00800080u; }
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// {lo, hi} as f16x2
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// d (+)= a [16 x 16] * b [16 x 8], fp16 operands, fp32 sums
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A query row's share of this lane: dims tq * D/4 .. + D/4 - 1 as fp32.
+template <int D>
+__device__ __forceinline__ void load_q(const float *row, int tq, float (&v)[D / 4]) {
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const float4 x = __ldg(reinterpret_cast<const float4 *>(row + tq * (D / 4)) + i);
+    v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
+  }
+}
+template <int D>
+__device__ __forceinline__ void load_q(const uint16_t *row, int tq, float (&v)[D / 4]) {
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    float x[8];
+    load8(row + tq * (D / 4) + 8 * i, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[8 * i + e] = x[e];
+  }
+}
+
+// The query operand. MMA column k of k-step s is dim tq * D/4 + 4 s + {0, 1}
+// (k = 2 tq, 2 tq + 1) and + {2, 3} (k = 2 tq + 8, + 9): a lane's operands of a
+// key row are then D/4 consecutive values, one or two whole scale blocks.
+//
+// Rows are brought to fp16 by a power of two that puts their largest magnitude
+// into [2^14, 2^15): bf16 queries are then exact down to 2^-24 / 2^15 of the
+// row's maximum, and fp32 queries keep 22 bits in a high and a low half (Q2).
+// `row` < 0 marks a row of zeros. Returns the inverse of the power of two.
+template <int D, typename T, bool Q2, int HALF>
+__device__ __forceinline__ float q_frag(const T *q, bool live, int tq, uint32_t (&hi)[D / 16][4],
+                                        uint32_t (&lo)[Q2 ? D / 16 : 1][4]) {
+  float v[D / 4];
+  if (live) {
+    load_q<D>(q, tq, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) v[i] = 0.f;
+  }
+  float mx = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 4; ++i) mx = fmaxf(mx, fabsf(v[i]));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  const int e = max(1, static_cast<int>(__float_as_uint(mx) >> 23));
+  const int k = min(126, 141 - e);                   // mx * 2^k in [2^14, 2^15)
+  const float f = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float a = v[4 * s + 2 * i] * f, b = v[4 * s + 2 * i + 1] * f;
+      const uint32_t h = pack_f16(a, b);
+      hi[s][2 * i + HALF] = h;
+      if constexpr (Q2) {
+        const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        lo[s][2 * i + HALF] = pack_f16(a - r.x, b - r.y);
+      }
+    }
+  return __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+}
+
+// Raw scores (fp16 operands' units) of 16 query rows against eight keys: this
+// lane's key row starts at `codes` and `scales` in shared memory; column c of
+// the tile is the key of the lanes with lane / 4 == c.
+template <int D, int MT, bool Q2>
+__device__ __forceinline__ void score_tile(const uint8_t *codes, const uint8_t *scales, int tq,
+                                           const uint32_t (&hi)[MT][D / 16][4],
+                                           const uint32_t (&lo)[Q2 ? MT : 1][Q2 ? D / 16 : 1][4],
+                                           float (&c)[MT][4]) {
+  uint32_t w[D / 32];
+  uint32_t sb;
+  if constexpr (D == 64) {
+    const uint2 x = *reinterpret_cast<const uint2 *>(codes + tq * 8);
+    w[0] = x.x; w[1] = x.y;
+    sb = scales[tq];
+  } else {
+    const uint4 x = *reinterpret_cast<const uint4 *>(codes + tq * 16);
+    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    sb = *reinterpret_cast<const uint16_t *>(scales + tq * 2);
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const uint32_t sc = scale_f16(i < 2 ? sb : sb >> 8);
+    uint32_t h[4];
+    codes_f16(w[i], h);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = mul_f16x2(h[e], sc);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        mma(c[m], hi[m][2 * i + t], h[2 * t], h[2 * t + 1]);
+        if constexpr (Q2) mma(c[m], lo[m][2 * i + t], h[2 * t], h[2 * t + 1]);
+      }
+  }
+}
+
+// Untiled asynchronous copy (a multiple of 16 bytes, both ends 16-byte
+// aligned) into shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          sm100::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(sm100::smem_u32(bar))
+      : "memory");
+}
+
+// Bounded wait of every lane of a warp, given up early when *abort is set.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const int *abort) {
+  if (sm100::mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = sm100::global_ns();
+  for (;;) {
+    if (sm100::mbar_try_wait_sleep(bar, parity, sm100::kSuspendHintNs)) return true;
+    if (*reinterpret_cast<const volatile int *>(abort) != 0) return false;
+    if (sm100::global_ns() - t0 > sm100::kWaitLimitNs) return false;
+  }
+}
+
+// A sequence's length in [0, min(cap, max_l_kv)]; a violation is recorded by
+// the thread with `report`.
+__device__ __forceinline__ int64_t length(const Q4Params &p, int b, bool report) {
+  int64_t L = p.l_kv[b];
+  const int64_t hi = p.cap < p.max_l_kv ? p.cap : p.max_l_kv;
+  if (L < 0 || L > hi) {
+    if (report) atomicOr(p.err, L < 0 ? SAGA_DEVERR_LKV_NEGATIVE : SAGA_DEVERR_LKV_TOO_LONG);
+    L = L < 0 ? 0 : hi;
+  }
+  return L;
+}
+
+}  // namespace q4
+}  // namespace saga

@@ -1,0 +1,293 @@
+// C ABI of the 4-bit cache calls (saga_q4.h): argument checks, the work plan
+// and the kernel launches. Nothing here allocates device memory or
+// synchronises.
+#include <cmath>
+
+#include "plan.h"
+#include "q4.cuh"
+#include "q4_kernels.h"
+#include "saga_q4.h"
+
+namespace saga {
+namespace {
+
+saga_status check_q4_shape(const saga_shape *shape) {
+  const saga_status r = check_shape(shape);
+  if (r != SAGA_OK) return r;
+  const saga_shape &s = *shape;
+  // 16-byte aligned rows of scales and codes, whole groups of four rows
+  if (s.k_stride_b % 256 != 0 || s.k_stride_h % 256 != 0 || s.v_stride_b % 256 != 0 ||
+      s.v_stride_h % 256 != 0 || s.cap % 4 != 0)
+    return SAGA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(s.B) * (s.h_k + s.h_v) > 65535) return SAGA_ERR_UNSUPPORTED;
+  return SAGA_OK;
+}
+
+saga_status check_cache(const saga_q4_cache *c) {
+  if (c == nullptr) return SAGA_ERR_INVALID_ARG;
+  for (const void *x : {c->k_codes, c->k_scales, c->v_codes, c->v_scales})
+    if (x == nullptr || !aligned(x, 16)) return SAGA_ERR_INVALID_ARG;
+  if (!aligned(c->k_g, 4) || !aligned(c->v_g, 4)) return SAGA_ERR_INVALID_ARG;
+  return SAGA_OK;
+}
+
+// Splits of equal length, a multiple of `chunk`: as many (b, kh, split) units as
+// fit on the GPU at once, for long rows in several waves of at most kMaxSplit
+// positions, so that ragged lengths balance.
+constexpr int64_t kMaxSplit = 16384;
+
+struct Q4Split {
+  int S;
+  int64_t split_len;
+};
+Q4Split split_rows(const saga_shape &s, int64_t chunk, int64_t ctas_per_sm) {
+  const int64_t rows = static_cast<int64_t>(s.B) * s.h_k;
+  const int64_t L = std::max<int64_t>(1, s.max_l_kv);
+  const int64_t slots = kSms * ctas_per_sm;
+  const int64_t waves = std::max<int64_t>(1, ceil_div(rows * L, slots * kMaxSplit));
+  const int64_t target = std::max<int64_t>(1, slots * waves / rows);
+  Q4Split q;
+  q.split_len = ceil_div(ceil_div(L, target), chunk) * chunk;
+  q.S = static_cast<int>(ceil_div(L, q.split_len));
+  return q;
+}
+
+// The Atop-N calls' plan (gather splits, lists, score rows, select buffers) is
+// that of the tensor-core step; the records of the dense call share the
+// gather's place.
+struct Q4Plan {
+  Plan step;
+  Q4Split dense, scan;
+  size_t shift;        // by which the step's offsets move up to make room for the dense records
+  size_t total;
+};
+Q4Plan q4_plan(const saga_shape &s) {
+  Q4Plan p;
+  saga_shape t = s;
+  t.dtype = SAGA_BF16;
+  p.step = make_plan(t, true);
+  p.scan = split_rows(s, kQ4ScanChunk, kQ4ScanCtasPerSm);
+  p.dense = {0, 0};
+  p.shift = 0;
+  if (dense_supports(s.h_q, s.h_k, s.h_v)) {
+    p.dense = split_rows(s, q4_dense_chunk(s.h_k, s.h_v), q4_dense_ctas_per_sm(s.d, s.h_q, s.h_k, s.h_v));
+    const size_t rec = static_cast<size_t>(s.d + kRecPad) * sizeof(float);
+    const size_t need = align_up(kAlign + static_cast<size_t>(s.B) * s.h_q * p.dense.S * rec);
+    if (need > p.step.off_lmask) p.shift = need - p.step.off_lmask;
+  }
+  p.total = p.step.total + p.shift;
+  return p;
+}
+
+saga_status check_q4_ws(const Q4Plan &pl, void *ws, size_t ws_bytes) {
+  if (ws == nullptr || !aligned(ws, kAlign) || ws_bytes < pl.total) return SAGA_ERR_WORKSPACE;
+  return SAGA_OK;
+}
+
+saga_status check_q4_inputs(const saga_q4_cache *cache, const void *q, const int32_t *l_kv) {
+  const saga_status r = check_cache(cache);
+  if (r != SAGA_OK) return r;
+  if (q == nullptr || l_kv == nullptr || !aligned(q, 16) || !aligned(l_kv, 4))
+    return SAGA_ERR_INVALID_ARG;
+  return SAGA_OK;
+}
+
+Q4Params base_params(const saga_shape &s, const Q4Plan &pl, const saga_q4_cache &c, const void *q,
+                     const int32_t *l_kv, void *ws) {
+  Q4Params p{};
+  char *wsb = static_cast<char *>(ws);
+  p.q = q;
+  p.kc = static_cast<const uint8_t *>(c.k_codes);
+  p.ks = static_cast<const uint8_t *>(c.k_scales);
+  p.vc = static_cast<const uint8_t *>(c.v_codes);
+  p.vs = static_cast<const uint8_t *>(c.v_scales);
+  p.k_g = c.k_g;
+  p.v_g = c.v_g;
+  p.l_kv = l_kv;
+  p.partials = reinterpret_cast<float *>(wsb + pl.step.off_partials);
+  p.lmask = reinterpret_cast<uint32_t *>(wsb + pl.step.off_lmask + pl.shift);
+  p.lscore = reinterpret_cast<float *>(wsb + pl.step.off_lscore + pl.shift);
+  p.nblk = pl.step.nblk;
+  p.err = static_cast<int32_t *>(ws);
+  p.abort = static_cast<int32_t *>(ws) + 1;
+  p.q_sb = s.q_stride_b; p.q_sh = s.q_stride_h;
+  p.kc_sb = s.k_stride_b / 2; p.kc_sh = s.k_stride_h / 2;
+  p.vc_sb = s.v_stride_b / 2; p.vc_sh = s.v_stride_h / 2;
+  p.cap = s.cap; p.max_l_kv = s.max_l_kv; p.row_stride = s.max_l_kv;
+  p.B = s.B; p.h_q = s.h_q; p.h_k = s.h_k; p.h_v = s.h_v;
+  p.scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(s.d)));
+  return p;
+}
+
+// The V half of a step, from the kept lists: gather, then combine.
+saga_status run_gather(const saga_shape &s, const Q4Plan &pl, const Q4Params &p, float *out,
+                       int32_t *sel_count, cudaStream_t st) {
+  GatherParams g{};
+  g.vc = p.vc; g.vs = p.vs; g.v_g = p.v_g;
+  g.v_sb = p.vc_sb; g.v_sh = p.vc_sh;
+  g.l_kv = p.l_kv; g.cap = p.cap; g.max_l_kv = p.max_l_kv;
+  g.lmask = p.lmask; g.lscore = p.lscore; g.nblk = p.nblk;
+  g.partials = p.partials; g.abort = p.abort; g.err = p.err;
+  g.B = s.B; g.h_q = s.h_q; g.SB = pl.step.SB; g.hpv = s.h_q / s.h_v;
+  g.blk_per_split = pl.step.blk_per_split;
+  const cudaError_t e = launch_gather(g, s.d, st);
+  if (e != cudaSuccess) return cuda_fail(e, "gather kernel (4-bit)");
+  return cuda_check(launch_combine(p.partials, p.l_kv, p.abort, out, sel_count, s.B, s.h_q, s.d,
+                                   pl.step.comb_S, pl.step.comb_split_len, s.cap, s.max_l_kv, st),
+                    "combine kernel");
+}
+
+}  // namespace
+}  // namespace saga
+
+using namespace saga;
+
+extern "C" {
+
+size_t saga_q4_workspace_size(const saga_shape *shape) {
+  if (check_q4_shape(shape) != SAGA_OK) return 0;
+  return q4_plan(*shape).total;
+}
+
+saga_status saga_q4_append_kv(const saga_shape *shape, const saga_q4_cache *cache, const void *k_new,
+                              const void *v_new, int32_t T, const int32_t *n_new, int32_t *l_kv,
+                              void *ws, size_t ws_bytes, saga_stream_t stream) {
+  saga_status r = check_q4_shape(shape);
+  if (r != SAGA_OK) return r;
+  const saga_shape &s = *shape;
+  if ((r = check_cache(cache)) != SAGA_OK) return r;
+  if (T < 1 || k_new == nullptr || v_new == nullptr || l_kv == nullptr) return SAGA_ERR_INVALID_ARG;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(l_kv, 4) || !aligned(n_new, 4))
+    return SAGA_ERR_INVALID_ARG;
+  if (ws == nullptr || !aligned(ws, kAlign) || ws_bytes < kAlign) return SAGA_ERR_WORKSPACE;
+  Q4Append p{};
+  p.k_new = k_new; p.v_new = v_new; p.n_new = n_new; p.l_kv = l_kv;
+  p.kc = static_cast<uint8_t *>(cache->k_codes); p.ks = static_cast<uint8_t *>(cache->k_scales);
+  p.vc = static_cast<uint8_t *>(cache->v_codes); p.vs = static_cast<uint8_t *>(cache->v_scales);
+  p.k_g = cache->k_g; p.v_g = cache->v_g;
+  p.err = static_cast<int32_t *>(ws);
+  p.kb_sb = s.k_stride_b / 16; p.kb_sh = s.k_stride_h / 16;
+  p.vb_sb = s.v_stride_b / 16; p.vb_sh = s.v_stride_h / 16;
+  p.cap = s.cap; p.B = s.B; p.T = T; p.h_k = s.h_k; p.h_v = s.h_v; p.d = s.d;
+  return cuda_check(launch_q4_append(p, s.dtype, reinterpret_cast<cudaStream_t>(stream)),
+                    "append kernel (4-bit)");
+}
+
+saga_status saga_q4_read_kv(const saga_shape *shape, const saga_q4_cache *cache, const int32_t *start,
+                            int64_t n, const int32_t *l_kv, void *K, void *V, void *ws,
+                            size_t ws_bytes, saga_stream_t stream) {
+  saga_status r = check_q4_shape(shape);
+  if (r != SAGA_OK) return r;
+  const saga_shape &s = *shape;
+  if ((r = check_cache(cache)) != SAGA_OK) return r;
+  if (n < 1 || l_kv == nullptr || K == nullptr || V == nullptr) return SAGA_ERR_INVALID_ARG;
+  if (!aligned(K, 16) || !aligned(V, 16) || !aligned(l_kv, 4) || !aligned(start, 4))
+    return SAGA_ERR_INVALID_ARG;
+  if (n > INT32_MAX) return SAGA_ERR_UNSUPPORTED;
+  if (ws == nullptr || !aligned(ws, kAlign) || ws_bytes < kAlign) return SAGA_ERR_WORKSPACE;
+  Q4Read p{};
+  p.kc = static_cast<const uint8_t *>(cache->k_codes); p.ks = static_cast<const uint8_t *>(cache->k_scales);
+  p.vc = static_cast<const uint8_t *>(cache->v_codes); p.vs = static_cast<const uint8_t *>(cache->v_scales);
+  p.k_g = cache->k_g; p.v_g = cache->v_g;
+  p.start = start; p.l_kv = l_kv; p.K = K; p.V = V;
+  p.err = static_cast<int32_t *>(ws);
+  p.kb_sb = s.k_stride_b / 16; p.kb_sh = s.k_stride_h / 16;
+  p.vb_sb = s.v_stride_b / 16; p.vb_sh = s.v_stride_h / 16;
+  p.cap = s.cap; p.n = n; p.B = s.B; p.h_k = s.h_k; p.h_v = s.h_v; p.d = s.d;
+  return cuda_check(launch_q4_read(p, s.dtype, reinterpret_cast<cudaStream_t>(stream)),
+                    "read kernel (4-bit)");
+}
+
+saga_status saga_q4_dense_decode(const saga_shape *shape, const saga_q4_cache *cache, const void *q,
+                                 const int32_t *l_kv, float *out, void *ws, size_t ws_bytes,
+                                 saga_stream_t stream) {
+  saga_status r = check_q4_shape(shape);
+  if (r != SAGA_OK) return r;
+  const saga_shape &s = *shape;
+  if (!dense_supports(s.h_q, s.h_k, s.h_v)) return SAGA_ERR_UNSUPPORTED;
+  if ((r = check_q4_inputs(cache, q, l_kv)) != SAGA_OK) return r;
+  if (out == nullptr || !aligned(out, 16)) return SAGA_ERR_INVALID_ARG;
+  const Q4Plan pl = q4_plan(s);
+  if ((r = check_q4_ws(pl, ws, ws_bytes)) != SAGA_OK) return r;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  Q4Params p = base_params(s, pl, *cache, q, l_kv, ws);
+  p.S = pl.dense.S;
+  p.split_len = pl.dense.split_len;
+  const cudaError_t e = launch_q4_dense(p, s.dtype, s.d, st);
+  if (e != cudaSuccess) return cuda_fail(e, "dense kernel (4-bit)");
+  return cuda_check(launch_combine(p.partials, l_kv, nullptr, out, nullptr, s.B, s.h_q, s.d, p.S,
+                                   p.split_len, s.cap, s.max_l_kv, st),
+                    "combine kernel");
+}
+
+saga_status saga_q4_decode_step(const saga_shape *shape, const saga_q4_cache *cache, const void *q,
+                                const int32_t *l_kv, const float *tau, float *out, int32_t *sel_count,
+                                uint8_t *sel_mask, void *ws, size_t ws_bytes, saga_stream_t stream) {
+  saga_status r = check_q4_shape(shape);
+  if (r != SAGA_OK) return r;
+  const saga_shape &s = *shape;
+  if ((r = check_q4_inputs(cache, q, l_kv)) != SAGA_OK) return r;
+  if (tau == nullptr || out == nullptr || !aligned(tau, 4) || !aligned(out, 16) || !aligned(sel_count, 4))
+    return SAGA_ERR_INVALID_ARG;
+  const Q4Plan pl = q4_plan(s);
+  if ((r = check_q4_ws(pl, ws, ws_bytes)) != SAGA_OK) return r;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  Q4Params p = base_params(s, pl, *cache, q, l_kv, ws);
+  p.S = pl.scan.S;
+  p.split_len = pl.scan.split_len;
+  p.tau = tau;
+  p.sel_mask = sel_mask;
+  const cudaError_t e = launch_q4_scan(p, false, s.dtype, s.d, st);
+  if (e != cudaSuccess) return cuda_fail(e, "scan kernel (4-bit)");
+  return run_gather(s, pl, p, out, sel_count, st);
+}
+
+saga_status saga_q4_refresh_threshold(const saga_shape *shape, const saga_q4_cache *cache, const void *q,
+                                      const int32_t *l_kv, int32_t N, float *tau, float *out,
+                                      int32_t *sel_count, uint8_t *sel_mask, float *scores, void *ws,
+                                      size_t ws_bytes, saga_stream_t stream) {
+  saga_status r = check_q4_shape(shape);
+  if (r != SAGA_OK) return r;
+  const saga_shape &s = *shape;
+  if ((r = check_q4_inputs(cache, q, l_kv)) != SAGA_OK) return r;
+  if (N < 1 || tau == nullptr || !aligned(tau, 4) || !aligned(out, 16) || !aligned(sel_count, 4) ||
+      !aligned(scores, 4))
+    return SAGA_ERR_INVALID_ARG;
+  if (out == nullptr && (sel_count != nullptr || sel_mask != nullptr)) return SAGA_ERR_INVALID_ARG;
+  const Q4Plan pl = q4_plan(s);
+  if ((r = check_q4_ws(pl, ws, ws_bytes)) != SAGA_OK) return r;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  char *wsb = static_cast<char *>(ws) + pl.shift;
+  Q4Params p = base_params(s, pl, *cache, q, l_kv, ws);
+  p.S = pl.scan.S;
+  p.split_len = pl.scan.split_len;
+  // 1. score rows with the top-byte histogram of every row (the bucket counts
+  // and digit-1 histograms of the select follow it and are cleared with it)
+  float *rows = scores != nullptr ? scores : reinterpret_cast<float *>(wsb + pl.step.off_scores);
+  p.hist = reinterpret_cast<uint32_t *>(wsb + pl.step.off_hist);
+  cudaError_t e = cudaMemsetAsync(p.hist, 0, static_cast<size_t>(s.B) * s.h_q * (256 + 1 + 256) * sizeof(uint32_t), st);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync (histograms)");
+  p.scores_out = rows;
+  if ((e = launch_q4_scan(p, true, s.dtype, s.d, st)) != cudaSuccess)
+    return cuda_fail(e, "score dump kernel (4-bit)");
+  // 2. exact N-th largest per row
+  e = launch_radix_select(rows, s.max_l_kv, l_kv, N, tau, s.B, s.h_q, s.cap, s.max_l_kv, p.hist, nullptr,
+                          reinterpret_cast<uint32_t *>(wsb + pl.step.off_gcand),
+                          reinterpret_cast<uint32_t *>(wsb + pl.step.off_gcount),
+                          reinterpret_cast<uint32_t *>(wsb + pl.step.off_hist1), pl.step.gcap,
+                          static_cast<int>(kSms), st);
+  if (e != cudaSuccess) return cuda_fail(e, "radix select kernel");
+  if (out == nullptr) return SAGA_OK;
+  // 3. this step's selection and PV with the fresh tau: the kept lists from the
+  // K cache again (the same scores bit for bit; its 4.5 bits a value cost less
+  // than the stored rows' fp32 per query head), then the gather
+  p.hist = nullptr;
+  p.scores_out = nullptr;
+  p.tau = tau;
+  p.sel_mask = sel_mask;
+  if ((e = launch_q4_scan(p, false, s.dtype, s.d, st)) != cudaSuccess)
+    return cuda_fail(e, "scan kernel (4-bit)");
+  return run_gather(s, pl, p, out, sel_count, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,50 @@
+// Launchers of the 4-bit cache kernels (host side, internal to the library).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "saga.h"
+
+namespace saga {
+
+struct Q4Params;
+
+// Strides kb_*, vb_* in blocks of 16 values (8 bytes of codes, 1 of scales).
+struct Q4Append {
+  const void *k_new, *v_new;       // [B][T][h_k][d], [B][T][h_v][d]
+  const int32_t *n_new;            // nullable [B]
+  int32_t *l_kv;
+  uint8_t *kc, *ks, *vc, *vs;
+  const float *k_g, *v_g;
+  int32_t *err;
+  int64_t kb_sb, kb_sh, vb_sb, vb_sh, cap;
+  int32_t B, T, h_k, h_v, d;
+};
+struct Q4Read {
+  const uint8_t *kc, *ks, *vc, *vs;
+  const float *k_g, *v_g;
+  const int32_t *start, *l_kv;     // start nullable
+  void *K, *V;                     // [B][h_k][n][d], [B][h_v][n][d]
+  int32_t *err;
+  int64_t kb_sb, kb_sh, vb_sb, vb_sh, cap, n;
+  int32_t B, h_k, h_v, d;
+};
+
+cudaError_t launch_q4_append(const Q4Append &p, int dtype, cudaStream_t st);
+cudaError_t launch_q4_read(const Q4Read &p, int dtype, cudaStream_t st);
+
+// Full attention over grid (S, B * h_k): per-split records for the combine.
+// Head layouts as dense_supports.
+cudaError_t launch_q4_dense(const Q4Params &p, int dtype, int d, cudaStream_t st);
+// The dense kernel's chunk of positions (splits are multiples of it) and CTAs per SM.
+int q4_dense_chunk(int h_k, int h_v);
+int q4_dense_ctas_per_sm(int d, int h_q, int h_k, int h_v);
+
+// Score pass over grid (S, B * h_k): score rows and their top-byte histograms
+// (dump), or the kept lists of p.tau (step).
+cudaError_t launch_q4_scan(const Q4Params &p, bool dump, int dtype, int d, cudaStream_t st);
+constexpr int kQ4ScanChunk = 256;   // splits are multiples of it
+constexpr int kQ4ScanCtasPerSm = 3;
+
+}  // namespace saga
