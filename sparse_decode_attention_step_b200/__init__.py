@@ -324,7 +324,7 @@ def q4_workspace_size(shp):
 
 class Q4Workspace:
     """Device workspace for the q4 calls of one shape, allocated through torch;
-    its error word is zeroed."""
+    its error word is zeroed. Calls that use it run on its device."""
 
     def __init__(self, shp, device="cuda", stream=None):
         import torch
@@ -332,53 +332,62 @@ class Q4Workspace:
         if self.nbytes == 0:
             raise SagaError(SAGA_ERR_INVALID_ARG, "saga_q4_workspace_size")
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.device = self.buf.device.index
         workspace_init(self.buf, self.nbytes, stream)
 
     def data_ptr(self):
         return self.buf.data_ptr()
 
 
+def _q4(name, shp, cache, ws, stream, *args):
+    """Call `name`(shape, cache, args..., workspace, stream). Arguments are ints,
+    None or tensors; a tensor, or the workspace, on another device than the
+    current one is refused (a kernel launched here could not reach it)."""
+    import torch
+    dev = torch.cuda.current_device()
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    v = []
+    for x in (cache.k_codes, *args):
+        if isinstance(x, torch.Tensor):
+            if x.device.index != dev:
+                raise SagaError(SAGA_ERR_INVALID_ARG, name + " (a tensor that is not on the current device)")
+            x = x.data_ptr()
+        v.append(x)
+    if getattr(ws, "device", dev) != dev:
+        raise SagaError(SAGA_ERR_INVALID_ARG, name + " (a workspace that is not on the current device)")
+    rc = getattr(_lib or load(), name)(shp, cache.c, *v[1:], ws.data_ptr(), ws.nbytes, stream)
+    if rc != SAGA_OK:
+        raise SagaError(rc, name)
+
+
 def q4_append_kv(shp, cache, k_new, v_new, T, l_kv, ws, n_new=None, stream=None):
     """Quantise T new rows per sequence (n_new[b] of them where given), k_new
     [B][T][h_k][d] and v_new [B][T][h_v][d], write them at position l_kv[b]
     and grow l_kv."""
-    p, n = _ws(ws)
-    _check(load().saga_q4_append_kv(ctypes.byref(shp), ctypes.byref(cache.c), _ptr(k_new),
-                                    _ptr(v_new), T, _ptr(n_new), _ptr(l_kv), p, n,
-                                    _stream(stream)), "saga_q4_append_kv")
+    _q4("saga_q4_append_kv", shp, cache, ws, stream, k_new, v_new, T, n_new, l_kv)
 
 
 def q4_read_kv(shp, cache, n, l_kv, K, V, ws, start=None, stream=None):
     """Rows start[b] .. start[b] + n - 1 of every head into K [B][h_k][n][d] and
     V [B][h_v][n][d]; rows at or behind l_kv[b] are left as they were."""
-    p, nb = _ws(ws)
-    _check(load().saga_q4_read_kv(ctypes.byref(shp), ctypes.byref(cache.c), _ptr(start), n,
-                                  _ptr(l_kv), _ptr(K), _ptr(V), p, nb, _stream(stream)),
-           "saga_q4_read_kv")
+    _q4("saga_q4_read_kv", shp, cache, ws, stream, start, n, l_kv, K, V)
 
 
 def q4_dense_decode(shp, cache, q, l_kv, out, ws, stream=None):
     """Full attention over a 4-bit cache, with the shape's key and value head maps."""
-    p, n = _ws(ws)
-    _check(load().saga_q4_dense_decode(ctypes.byref(shp), ctypes.byref(cache.c), _ptr(q),
-                                       _ptr(l_kv), _ptr(out), p, n, _stream(stream)),
-           "saga_q4_dense_decode")
+    _q4("saga_q4_dense_decode", shp, cache, ws, stream, q, l_kv, out)
 
 
 def q4_decode_step(shp, cache, q, l_kv, tau, out, ws, sel_count=None, sel_mask=None, stream=None):
     """One Atop-N step with stored thresholds over a 4-bit cache."""
-    p, n = _ws(ws)
-    _check(load().saga_q4_decode_step(ctypes.byref(shp), ctypes.byref(cache.c), _ptr(q),
-                                      _ptr(l_kv), _ptr(tau), _ptr(out), _ptr(sel_count),
-                                      _ptr(sel_mask), p, n, _stream(stream)),
-           "saga_q4_decode_step")
+    _q4("saga_q4_decode_step", shp, cache, ws, stream, q, l_kv, tau, out, sel_count, sel_mask)
 
 
 def q4_refresh_threshold(shp, cache, q, l_kv, N, tau, ws, out=None, sel_count=None, sel_mask=None,
                          scores=None, stream=None):
     """Exact N-th largest scores over a 4-bit cache into tau; with out, the step too."""
-    p, n = _ws(ws)
-    _check(load().saga_q4_refresh_threshold(ctypes.byref(shp), ctypes.byref(cache.c), _ptr(q),
-                                            _ptr(l_kv), N, _ptr(tau), _ptr(out), _ptr(sel_count),
-                                            _ptr(sel_mask), _ptr(scores), p, n, _stream(stream)),
-           "saga_q4_refresh_threshold")
+    _q4("saga_q4_refresh_threshold", shp, cache, ws, stream, q, l_kv, N, tau, out, sel_count,
+        sel_mask, scores)

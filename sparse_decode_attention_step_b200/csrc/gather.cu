@@ -25,7 +25,7 @@
 //
 // A 4-bit cache (Q4) stages a row as its codes and its scales, D/2 and D/16
 // bytes, and converts them when it folds; the values' common factor goes into
-// the CTA's record.
+// the CTA's record. Its scan leaves a kept score at its position in the block.
 //
 // A scan that gave up on a bounded wait sets the step's abort word; this
 // kernel then writes poisoned records (m = +inf, count = -1), which the
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 8) gather_kernel(const GatherParams 
                 const int w = c - D / 32;
                 sm100::cp_async4(row + D / 2 + w * 4, xg + t * (D / 16) + w * 4);
               } else if (c == LPG - 1) {
-                sm100::cp_async4(sst + i, sg + bl * 32 + (en & 31));
+                sm100::cp_async4(sst + i, sg + t);       // at its position, not at its rank
               }
             } else {
               sm100::cp_async16(vst + i * C::kRowBytes + c * 16, vg + t * D);

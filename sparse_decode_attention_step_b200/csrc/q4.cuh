@@ -27,10 +27,11 @@ struct Q4Params {
   const float *tau;
   float *partials;             // [B][h_q][S][d + kRecPad] (dense)
   float *scores_out;           // dump: [B][h_q][row_stride]
+  float *group_max;            // max: [B * h_q][nblk * 4], largest scores of 8-position groups
+  int32_t *n_groups;           // max: [B] groups of each row
   uint8_t *sel_mask;           // nullable [B][h_q][row_stride]
-  uint32_t *hist;              // dump: [B][h_q][256] top-byte histograms
-  uint32_t *lmask;             // step: the kept lists, as in StepParams
-  float *lscore;
+  uint32_t *lmask;             // step: [B * h_q][nblk] kept positions of every 32-position block
+  float *lscore;               // [B * h_q][nblk * 32] kept scores, each at its position
   int64_t nblk;
   int32_t *err, *abort;
   int64_t q_sb, q_sh;          // elements

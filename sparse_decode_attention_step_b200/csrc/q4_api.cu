@@ -52,14 +52,13 @@ Q4Split split_rows(const saga_shape &s, int64_t chunk, int64_t ctas_per_sm) {
   return q;
 }
 
-// The Atop-N calls' plan (gather splits, lists, score rows, select buffers) is
-// that of the tensor-core step; the records of the dense call share the
-// gather's place.
+// Workspace: error and abort words, the records of the dense call or of the
+// gather (whose splits are those of the tensor-core step), the kept lists, and
+// for the refresh the group maxima, their counts and lower bounds.
 struct Q4Plan {
   Plan step;
   Q4Split dense, scan;
-  size_t shift;        // by which the step's offsets move up to make room for the dense records
-  size_t total;
+  size_t off_records, off_lmask, off_lscore, off_gmax, off_ngroups, off_bound, total;
 };
 Q4Plan q4_plan(const saga_shape &s) {
   Q4Plan p;
@@ -68,14 +67,17 @@ Q4Plan q4_plan(const saga_shape &s) {
   p.step = make_plan(t, true);
   p.scan = split_rows(s, kQ4ScanChunk, kQ4ScanCtasPerSm);
   p.dense = {0, 0};
-  p.shift = 0;
-  if (dense_supports(s.h_q, s.h_k, s.h_v)) {
+  if (dense_supports(s.h_q, s.h_k, s.h_v))
     p.dense = split_rows(s, q4_dense_chunk(s.h_k, s.h_v), q4_dense_ctas_per_sm(s.d, s.h_q, s.h_k, s.h_v));
-    const size_t rec = static_cast<size_t>(s.d + kRecPad) * sizeof(float);
-    const size_t need = align_up(kAlign + static_cast<size_t>(s.B) * s.h_q * p.dense.S * rec);
-    if (need > p.step.off_lmask) p.shift = need - p.step.off_lmask;
-  }
-  p.total = p.step.total + p.shift;
+  const size_t rec = static_cast<size_t>(s.d + kRecPad) * sizeof(float);
+  const size_t rows = static_cast<size_t>(s.B) * s.h_q, lists = rows * p.step.nblk;
+  p.off_records = kAlign;
+  p.off_lmask = align_up(p.off_records + rows * std::max(p.dense.S, p.step.comb_S) * rec);
+  p.off_lscore = align_up(p.off_lmask + lists * sizeof(uint32_t));
+  p.off_gmax = align_up(p.off_lscore + lists * 32 * sizeof(float));
+  p.off_ngroups = align_up(p.off_gmax + lists * 4 * sizeof(float));
+  p.off_bound = align_up(p.off_ngroups + s.B * sizeof(int32_t));
+  p.total = align_up(p.off_bound + rows * sizeof(float));
   return p;
 }
 
@@ -104,9 +106,11 @@ Q4Params base_params(const saga_shape &s, const Q4Plan &pl, const saga_q4_cache 
   p.k_g = c.k_g;
   p.v_g = c.v_g;
   p.l_kv = l_kv;
-  p.partials = reinterpret_cast<float *>(wsb + pl.step.off_partials);
-  p.lmask = reinterpret_cast<uint32_t *>(wsb + pl.step.off_lmask + pl.shift);
-  p.lscore = reinterpret_cast<float *>(wsb + pl.step.off_lscore + pl.shift);
+  p.partials = reinterpret_cast<float *>(wsb + pl.off_records);
+  p.lmask = reinterpret_cast<uint32_t *>(wsb + pl.off_lmask);
+  p.lscore = reinterpret_cast<float *>(wsb + pl.off_lscore);
+  p.group_max = reinterpret_cast<float *>(wsb + pl.off_gmax);
+  p.n_groups = reinterpret_cast<int32_t *>(wsb + pl.off_ngroups);
   p.nblk = pl.step.nblk;
   p.err = static_cast<int32_t *>(ws);
   p.abort = static_cast<int32_t *>(ws) + 1;
@@ -237,7 +241,7 @@ saga_status saga_q4_decode_step(const saga_shape *shape, const saga_q4_cache *ca
   p.split_len = pl.scan.split_len;
   p.tau = tau;
   p.sel_mask = sel_mask;
-  const cudaError_t e = launch_q4_scan(p, false, s.dtype, s.d, st);
+  const cudaError_t e = launch_q4_scan(p, kQ4Step, s.dtype, s.d, st);
   if (e != cudaSuccess) return cuda_fail(e, "scan kernel (4-bit)");
   return run_gather(s, pl, p, out, sel_count, st);
 }
@@ -257,37 +261,32 @@ saga_status saga_q4_refresh_threshold(const saga_shape *shape, const saga_q4_cac
   const Q4Plan pl = q4_plan(s);
   if ((r = check_q4_ws(pl, ws, ws_bytes)) != SAGA_OK) return r;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  char *wsb = static_cast<char *>(ws) + pl.shift;
   Q4Params p = base_params(s, pl, *cache, q, l_kv, ws);
   p.S = pl.scan.S;
   p.split_len = pl.scan.split_len;
-  // 1. score rows with the top-byte histogram of every row (the bucket counts
-  // and digit-1 histograms of the select follow it and are cleared with it)
-  float *rows = scores != nullptr ? scores : reinterpret_cast<float *>(wsb + pl.step.off_scores);
-  p.hist = reinterpret_cast<uint32_t *>(wsb + pl.step.off_hist);
-  cudaError_t e = cudaMemsetAsync(p.hist, 0, static_cast<size_t>(s.B) * s.h_q * (256 + 1 + 256) * sizeof(uint32_t), st);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync (histograms)");
-  p.scores_out = rows;
-  if ((e = launch_q4_scan(p, true, s.dtype, s.d, st)) != cudaSuccess)
-    return cuda_fail(e, "score dump kernel (4-bit)");
-  // 2. exact N-th largest per row
-  e = launch_radix_select(rows, s.max_l_kv, l_kv, N, tau, s.B, s.h_q, s.cap, s.max_l_kv, p.hist, nullptr,
-                          reinterpret_cast<uint32_t *>(wsb + pl.step.off_gcand),
-                          reinterpret_cast<uint32_t *>(wsb + pl.step.off_gcount),
-                          reinterpret_cast<uint32_t *>(wsb + pl.step.off_hist1), pl.step.gcap,
-                          static_cast<int>(kSms), st);
+  cudaError_t e;
+  if (scores != nullptr) {
+    p.scores_out = scores;
+    if ((e = launch_q4_scan(p, kQ4Dump, s.dtype, s.d, st)) != cudaSuccess)
+      return cuda_fail(e, "score dump kernel (4-bit)");
+  }
+  // 1. the largest score of every eight positions, and the N-th largest of those:
+  // a lower bound of the threshold (-inf with N groups or fewer)
+  if ((e = launch_q4_scan(p, kQ4Max, s.dtype, s.d, st)) != cudaSuccess)
+    return cuda_fail(e, "group maximum kernel (4-bit)");
+  float *bound = reinterpret_cast<float *>(static_cast<char *>(ws) + pl.off_bound);
+  const int64_t groups = p.nblk * 4;
+  e = launch_radix_select(p.group_max, groups, p.n_groups, N, bound, s.B, s.h_q, groups, groups, nullptr,
+                          nullptr, nullptr, nullptr, nullptr, 0, static_cast<int>(kSms), st);
   if (e != cudaSuccess) return cuda_fail(e, "radix select kernel");
-  if (out == nullptr) return SAGA_OK;
-  // 3. this step's selection and PV with the fresh tau: the kept lists from the
-  // K cache again (the same scores bit for bit; its 4.5 bits a value cost less
-  // than the stored rows' fp32 per query head), then the gather
-  p.hist = nullptr;
-  p.scores_out = nullptr;
-  p.tau = tau;
-  p.sel_mask = sel_mask;
-  if ((e = launch_q4_scan(p, false, s.dtype, s.d, st)) != cudaSuccess)
+  // 2. the scores that reach it
+  p.tau = bound;
+  if ((e = launch_q4_scan(p, kQ4Step, s.dtype, s.d, st)) != cudaSuccess)
     return cuda_fail(e, "scan kernel (4-bit)");
-  return run_gather(s, pl, p, out, sel_count, st);
+  // 3. their N-th largest; for the step, the lists cut down to it
+  if ((e = launch_q4_select(p, N, tau, out != nullptr, sel_mask, st)) != cudaSuccess)
+    return cuda_fail(e, "select kernel (4-bit)");
+  return out == nullptr ? SAGA_OK : run_gather(s, pl, p, out, sel_count, st);
 }
 
 }  // extern "C"

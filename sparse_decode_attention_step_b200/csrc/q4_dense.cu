@@ -135,11 +135,11 @@ q4_dense_kernel(const Q4Params p) {
         }
       }
       if (c < nchunks) {
-        // gave up: the copies in flight land before the CTA can exit
         atomicOr(p.err, SAGA_DEVERR_TIMEOUT);
         *reinterpret_cast<volatile int *>(&s_abort) = 1;
-        for (int i = c > ST ? c - ST : 0; i < c; ++i) sm100::mbar_wait(&s_full[i % ST], (i / ST) & 1);
       }
+      // the copies in flight land before the ring is used again
+      for (int i = c > ST ? c - ST : 0; i < c; ++i) sm100::mbar_wait(&s_full[i % ST], (i / ST) & 1);
     }
     __syncwarp();
   }

@@ -41,10 +41,16 @@ cudaError_t launch_q4_dense(const Q4Params &p, int dtype, int d, cudaStream_t st
 int q4_dense_chunk(int h_k, int h_v);
 int q4_dense_ctas_per_sm(int d, int h_q, int h_k, int h_v);
 
-// Score pass over grid (S, B * h_k): score rows and their top-byte histograms
-// (dump), or the kept lists of p.tau (step).
-cudaError_t launch_q4_scan(const Q4Params &p, bool dump, int dtype, int d, cudaStream_t st);
+// Score pass over grid (S, B * h_k): the kept lists of p.tau (step), the group
+// maxima and group counts (max), or the score rows (dump).
+enum { kQ4Step = 0, kQ4Max = 1, kQ4Dump = 2 };
+cudaError_t launch_q4_scan(const Q4Params &p, int mode, int dtype, int d, cudaStream_t st);
 constexpr int kQ4ScanChunk = 256;   // splits are multiples of it
 constexpr int kQ4ScanCtasPerSm = 3;
+
+// tau[b][j] = the N-th largest of row (b, j)'s listed scores, or -inf when
+// N >= l_kv[b]; with `keep`, the lists (and a given sel_mask) are cut down to it.
+cudaError_t launch_q4_select(const Q4Params &p, int32_t N, float *tau, bool keep, uint8_t *sel_mask,
+                             cudaStream_t st);
 
 }  // namespace saga

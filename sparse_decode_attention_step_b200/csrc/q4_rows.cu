@@ -2,9 +2,11 @@
 //
 // A block of 16 values x is stored as e4m3(max|x| / (6 g)) and 16 e2m1 codes
 // of x / (scale g); see saga_q4.h. One thread quantises one block: the maximum,
-// one division for the scale, 16 for the codes (true divisions, so that values
-// on a rounding border go where the definition says), and the hardware's
-// conversions, which round to nearest even.
+// one division for the scale, 16 correctly rounded quotients for the codes (so
+// that values on a rounding border go where the definition says), and the
+// hardware's conversions, which round to nearest even. Both kernels move each
+// byte once and are bound by how many loads a CTA keeps in flight, so a thread
+// loads several blocks before it converts the first.
 #include "kernels.h"
 #include "q4.cuh"
 #include "q4_kernels.h"
@@ -14,6 +16,9 @@ namespace saga {
 namespace {
 
 constexpr int kThreads = 256;
+template <typename T>
+constexpr int kAppendBlocks = sizeof(T) == 2 ? 4 : 2;      // blocks of 16 a thread: 128 bytes in flight
+constexpr int kReadPieces = 8;                             // pieces of 8 values a thread
 
 __device__ __forceinline__ uint32_t e4m3(float x) {           // x in [0, 448]
   uint16_t d;
@@ -36,32 +41,77 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
   return d;
 }
 
-template <typename T>
-__device__ __forceinline__ void load16(const T *p, float (&x)[16]) {
-  float a[8], b[8];
-  load8(p, a);
-  load8(p + 8, b);
+// x >= 0 over t, correctly rounded, by Markstein's method (IBM J. Res. Dev. 34,
+// 1990): with `inv` the rounded reciprocal, one correction makes the quotient
+// faithful and a second one from its exact residual rounds it correctly. For t
+// within 2^+-100 the residuals neither overflow nor lose bits that matter (a
+// quotient small enough for that rounds to code 0 all the same). An infinite x
+// gives NaN, which fminf turns into 6, the largest code.
+__device__ __forceinline__ float quotient(float x, float t, float inv) {
+  float q = x * inv;
+  q = fmaf(fmaf(-q, t, x), inv, q);
+  return fmaf(fmaf(-q, t, x), inv, q);
+}
+
+// A thread's raw block of 16 values, loaded ahead of its conversion.
+struct Raw16 {
+  uint4 w[4];
+};
+__device__ __forceinline__ void load_raw(const uint16_t *p, Raw16 &r) {
+  r.w[0] = __ldg(reinterpret_cast<const uint4 *>(p));
+  r.w[1] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+}
+__device__ __forceinline__ void load_raw(const float *p, Raw16 &r) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) { x[i] = a[i]; x[8 + i] = b[i]; }
+  for (int i = 0; i < 4; ++i) r.w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+}
+template <typename T>
+__device__ __forceinline__ void widen(const Raw16 &r, float (&x)[16]) {
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t u[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) { x[8 * i + 2 * e] = bf16lo(u[e]); x[8 * i + 2 * e + 1] = bf16hi(u[e]); }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[4 * i] = __uint_as_float(r.w[i].x); x[4 * i + 1] = __uint_as_float(r.w[i].y);
+      x[4 * i + 2] = __uint_as_float(r.w[i].z); x[4 * i + 3] = __uint_as_float(r.w[i].w);
+    }
+  }
 }
 
 template <typename T>
-__device__ __forceinline__ void quantise_block(const T *src, float g, uint2 *codes, uint8_t *scale) {
+__device__ __forceinline__ void quantise_block(const Raw16 &raw, float g, uint2 *codes, uint8_t *scale) {
   float x[16];
-  load16(src, x);
+  widen<T>(raw, x);
   float mx = 0.f;
+  uint32_t sign[2] = {0u, 0u};
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     if (x[i] != x[i]) x[i] = 0.f;                            // NaN counts as zero
-    mx = fmaxf(mx, fabsf(x[i]));
+    sign[i / 8] |= (__float_as_uint(x[i]) >> 31) << (i % 8 * 4 + 3);
+    x[i] = fabsf(x[i]);
+    mx = fmaxf(mx, x[i]);
   }
   const uint32_t s = e4m3(fminf(448.f, __fdiv_rn(mx, __fmul_rn(6.f, g))));
   const float t = __fmul_rn(e4m3_value(s), g);
   uint32_t w[2] = {0u, 0u};
   if (s != 0u) {
+    if (t > 0x1p-100f && t < 0x1p100f) {
+      const float inv = __frcp_rn(t);
 #pragma unroll
-    for (int i = 0; i < 16; i += 2)
-      w[i / 8] |= e2m1x2(__fdiv_rn(x[i], t), __fdiv_rn(x[i + 1], t)) << (i % 8 * 4);
+      for (int i = 0; i < 16; ++i) x[i] = fminf(quotient(x[i], t, inv), 6.f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = fminf(__fdiv_rn(x[i], t), 6.f);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) w[i / 8] |= e2m1x2(x[i], x[i + 1]) << (i % 8 * 4);
+    w[0] |= sign[0];
+    w[1] |= sign[1];
   }
   *codes = make_uint2(w[0], w[1]);
   *scale = static_cast<uint8_t>(s);
@@ -79,22 +129,36 @@ __device__ __forceinline__ int64_t append_rows(const Q4Append &p, int b, int64_t
   return bad != 0 ? 0 : n;
 }
 
-// Block i of a head's n new rows, in position order.
+// Blocks of a head's n new rows, in position order: where block i comes from
+// and goes to.
 template <typename T>
-__device__ __forceinline__ void append_block(const Q4Append &p, int b, int hh, int64_t at, int64_t i) {
-  const bool is_v = hh >= p.h_k;
-  const int h = is_v ? hh - p.h_k : hh, heads = is_v ? p.h_v : p.h_k;
-  const int bpr = p.d / 16;
-  const int64_t r = i / bpr;
-  const int w = static_cast<int>(i % bpr);
-  const T *src = static_cast<const T *>(is_v ? p.v_new : p.k_new) +
-                 ((static_cast<int64_t>(b) * p.T + r) * heads + h) * p.d + w * 16;
-  const float *gp = is_v ? p.v_g : p.k_g;
-  // codes: 8 bytes a block, scales: 1
-  const int64_t blk = (is_v ? b * p.vb_sb + h * p.vb_sh : b * p.kb_sb + h * p.kb_sh) + (at + r) * bpr + w;
-  quantise_block(src, gp != nullptr ? gp[h] : 1.f,
-                 reinterpret_cast<uint2 *>(is_v ? p.vc : p.kc) + blk, (is_v ? p.vs : p.ks) + blk);
-}
+struct AppendHead {
+  const T *src;
+  uint8_t *codes, *scales;
+  int64_t src_row, first;      // elements between the head's new rows; first block of row l_kv[b]
+  float g;
+  int bpr;                     // blocks per row
+
+  __device__ __forceinline__ AppendHead(const Q4Append &p, int b, int hh, int64_t at) {
+    const bool is_v = hh >= p.h_k;
+    const int h = is_v ? hh - p.h_k : hh, heads = is_v ? p.h_v : p.h_k;
+    bpr = p.d / 16;
+    src_row = static_cast<int64_t>(heads) * p.d;
+    src = static_cast<const T *>(is_v ? p.v_new : p.k_new) + static_cast<int64_t>(b) * p.T * src_row + h * p.d;
+    codes = is_v ? p.vc : p.kc;
+    scales = is_v ? p.vs : p.ks;
+    first = (is_v ? b * p.vb_sb + h * p.vb_sh : b * p.kb_sb + h * p.kb_sh) + at * bpr;
+    const float *gp = is_v ? p.v_g : p.k_g;
+    g = gp != nullptr ? __ldg(gp + h) : 1.f;
+  }
+  // i / bpr by a shift: bpr is 4 or 8
+  __device__ __forceinline__ const T *from(int64_t i) const {
+    return src + (i >> (bpr == 4 ? 2 : 3)) * src_row + (i & (bpr - 1)) * 16;
+  }
+  __device__ __forceinline__ void put(int64_t i, const Raw16 &raw) const {
+    quantise_block<T>(raw, g, reinterpret_cast<uint2 *>(codes) + first + i, scales + first + i);
+  }
+};
 
 // Few rows: one CTA per sequence writes them all, then its length.
 template <typename T>
@@ -104,9 +168,13 @@ __global__ void __launch_bounds__(kThreads) q4_append_small_kernel(const Q4Appen
   const int b = blockIdx.x;
   int64_t at;
   const int64_t n = append_rows(p, b, &at, threadIdx.x == 0);
-  const int64_t per_head = n * (p.d / 16);
-  for (int64_t i = threadIdx.x; i < per_head * (p.h_k + p.h_v); i += kThreads)
-    append_block<T>(p, b, static_cast<int>(i / per_head), at, i % per_head);
+  const int per_head = static_cast<int>(n) * (p.d / 16);
+  for (int i = threadIdx.x; i < per_head * (p.h_k + p.h_v); i += kThreads) {
+    const AppendHead<T> h(p, b, i / per_head, at);
+    Raw16 raw;
+    load_raw(h.from(i % per_head), raw);
+    h.put(i % per_head, raw);
+  }
   __syncthreads();
   if (threadIdx.x == 0 && n > 0) p.l_kv[b] = static_cast<int32_t>(at + n);
 }
@@ -115,13 +183,22 @@ __global__ void __launch_bounds__(kThreads) q4_append_small_kernel(const Q4Appen
 // follow in a launch of their own, when every CTA has read them.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) q4_append_kernel(const Q4Append p) {
+  constexpr int U = kAppendBlocks<T>;
   pdl_wait();
   pdl_trigger();
   const int hh = blockIdx.y % (p.h_k + p.h_v), b = blockIdx.y / (p.h_k + p.h_v);
   int64_t at;
-  const int64_t n = append_rows(p, b, &at, blockIdx.x == 0 && hh == 0 && threadIdx.x == 0);
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i < n * (p.d / 16)) append_block<T>(p, b, hh, at, i);
+  const int64_t n = append_rows(p, b, &at, blockIdx.x == 0 && hh == 0 && threadIdx.x == 0) * (p.d / 16);
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * U) + threadIdx.x;
+  if (i0 >= n) return;
+  const AppendHead<T> h(p, b, hh, at);
+  Raw16 raw[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (i0 + u * kThreads < n) load_raw(h.from(i0 + u * kThreads), raw[u]);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (i0 + u * kThreads < n) h.put(i0 + u * kThreads, raw[u]);
 }
 
 __global__ void q4_grow_kernel(const Q4Append p) {
@@ -146,9 +223,11 @@ __device__ __forceinline__ void store8(uint16_t *p, const float (&x)[8]) {
   *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One thread reads eight values of a row: four bytes of codes and their scale.
+// A thread reads kReadPieces pieces of eight values: four bytes of codes and
+// their scale each.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) q4_read_kernel(const Q4Read p) {
+  constexpr int U = kReadPieces;
   pdl_wait();
   pdl_trigger();
   const int hh = blockIdx.y % (p.h_k + p.h_v), b = blockIdx.y / (p.h_k + p.h_v);
@@ -158,31 +237,40 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(const Q4Read p) {
   if (blockIdx.x == 0 && hh == 0 && threadIdx.x == 0 && (l < 0 || t0 < 0 || l > p.cap))
     atomicOr(p.err, l < 0 || t0 < 0 ? SAGA_DEVERR_LKV_NEGATIVE : SAGA_DEVERR_LKV_TOO_LONG);
   if (t0 < 0) return;
-  const int64_t L = l < p.cap ? l : p.cap;
+  const int64_t rows = min(p.n, (l < p.cap ? l : p.cap) - t0);   // rows of the window that exist
   const int ppr = p.d / 8;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t r = i / ppr;
-  const int w = static_cast<int>(i % ppr);
-  if (r >= p.n || t0 + r >= L) return;
-  const int64_t word = (is_v ? b * p.vb_sb + h * p.vb_sh : b * p.kb_sb + h * p.kb_sh) * 2 +
-                       (t0 + r) * ppr + w;
-  uint32_t c[4];
-  q4::codes_f16(__ldg(reinterpret_cast<const uint32_t *>(is_v ? p.vc : p.kc) + word), c);
-  const uint32_t s = q4::scale_f16(__ldg((is_v ? p.vs : p.ks) + word / 2));
+  const int64_t n = rows * ppr;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (kThreads * U) + threadIdx.x;
+  if (i0 >= n) return;
+  const int64_t first = (is_v ? b * p.vb_sb + h * p.vb_sh : b * p.kb_sb + h * p.kb_sh) * 2 + t0 * ppr;
+  const uint32_t *codes = reinterpret_cast<const uint32_t *>(is_v ? p.vc : p.kc) + first;
+  const uint8_t *scales = (is_v ? p.vs : p.ks) + first / 2;      // first is even: rows are
   const float *gp = is_v ? p.v_g : p.k_g;
-  const float g = (gp != nullptr ? gp[h] : 1.f);
-  float x[8];
+  const float g = kQ4Unit * (gp != nullptr ? __ldg(gp + h) : 1.f);
+  T *out = static_cast<T *>(is_v ? p.V : p.K) + (static_cast<int64_t>(b) * heads + h) * p.n * p.d;
+  uint32_t w[U], s[U];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t v = q4::mul_f16x2(c[e], s);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v));
-    // the stored value is exact before g: one rounding to fp32
-    x[2 * e] = f.x * kQ4Unit * g;
-    x[2 * e + 1] = f.y * kQ4Unit * g;
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = i0 + u * kThreads;
+    if (i < n) { w[u] = __ldg(codes + i); s[u] = __ldg(scales + i / 2); }
   }
-  T *out = static_cast<T *>(is_v ? p.V : p.K) +
-           ((static_cast<int64_t>(b) * heads + h) * p.n + r) * p.d + w * 8;
-  store8(out, x);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = i0 + u * kThreads;
+    if (i >= n) break;
+    uint32_t c[4];
+    q4::codes_f16(w[u], c);
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t v = q4::mul_f16x2(c[e], q4::scale_f16(s[u]));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v));
+      // the stored value is exact before g: one rounding to fp32
+      x[2 * e] = f.x * g;
+      x[2 * e + 1] = f.y * g;
+    }
+    store8(out + i * 8, x);
+  }
 }
 
 }  // namespace
@@ -195,7 +283,8 @@ cudaError_t launch_q4_append(const Q4Append &p, int dtype, cudaStream_t st) {
     if (dtype == SAGA_BF16) return launch_pdl(q4_append_small_kernel<uint16_t>, dim3(p.B), dim3(kThreads), 0, st, p);
     return launch_pdl(q4_append_small_kernel<float>, dim3(p.B), dim3(kThreads), 0, st, p);
   }
-  const dim3 grid(static_cast<unsigned>((blocks + kThreads - 1) / kThreads), p.B * heads);
+  const int64_t per_cta = kThreads * (dtype == SAGA_BF16 ? kAppendBlocks<uint16_t> : kAppendBlocks<float>);
+  const dim3 grid(static_cast<unsigned>((blocks + per_cta - 1) / per_cta), p.B * heads);
   cudaError_t e = dtype == SAGA_BF16 ? launch_pdl(q4_append_kernel<uint16_t>, grid, dim3(kThreads), 0, st, p)
                                      : launch_pdl(q4_append_kernel<float>, grid, dim3(kThreads), 0, st, p);
   if (e != cudaSuccess) return e;
@@ -204,7 +293,8 @@ cudaError_t launch_q4_append(const Q4Append &p, int dtype, cudaStream_t st) {
 
 cudaError_t launch_q4_read(const Q4Read &p, int dtype, cudaStream_t st) {
   const int64_t pieces = p.n * (p.d / 8);
-  const dim3 grid(static_cast<unsigned>((pieces + kThreads - 1) / kThreads), p.B * (p.h_k + p.h_v));
+  const int64_t per_cta = kThreads * kReadPieces;
+  const dim3 grid(static_cast<unsigned>((pieces + per_cta - 1) / per_cta), p.B * (p.h_k + p.h_v));
   if (dtype == SAGA_BF16) return launch_pdl(q4_read_kernel<uint16_t>, grid, dim3(kThreads), 0, st, p);
   return launch_pdl(q4_read_kernel<float>, grid, dim3(kThreads), 0, st, p);
 }
