@@ -25,7 +25,8 @@ struct Q4Params {
   const float *k_g, *v_g;      // nullable [h_k], [h_v]
   const int32_t *l_kv;
   const float *tau;
-  float *partials;             // [B][h_q][S][d + kRecPad] (dense)
+  float *partials;             // dense: [S + B * h_k][h_q / h_k][d + kRecPad]
+  float *out;                  // dense: [B][h_q][d]
   float *scores_out;           // dump: [B][h_q][row_stride]
   float *group_max;            // max: [B * h_q][nblk * 4], largest scores of 8-position groups
   int32_t *n_groups;           // max: [B] groups of each row
@@ -36,8 +37,9 @@ struct Q4Params {
   int32_t *err, *abort;
   int64_t q_sb, q_sh;          // elements
   int64_t kc_sb, kc_sh, vc_sb, vc_sh;
-  int64_t cap, max_l_kv, row_stride, split_len;
-  int32_t B, h_q, h_k, h_v, S;
+  int64_t cap, max_l_kv, row_stride;
+  int32_t B, h_q, h_k, h_v;
+  int32_t S;                   // CTAs that share the rows
   float scale;                 // 1 / sqrt(d)
 };
 
@@ -208,8 +210,8 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const i
   }
 }
 
-// A sequence's length in [0, min(cap, max_l_kv)]; a violation is recorded by
-// the thread with `report`.
+// A sequence's length in [0, min(cap, max_l_kv)]; a violation is recorded where
+// `report` is set.
 __device__ __forceinline__ int64_t length(const Q4Params &p, int b, bool report) {
   int64_t L = p.l_kv[b];
   const int64_t hi = p.cap < p.max_l_kv ? p.cap : p.max_l_kv;
@@ -219,6 +221,149 @@ __device__ __forceinline__ int64_t length(const Q4Params &p, int b, bool report)
   }
   return L;
 }
+
+// How the rows (b, key head) are shared among CTAs: every row is a run of chunks
+// of CH positions, the rows follow one another, and CTA i of n takes the chunks
+// from floor(i T / n) to floor((i + 1) T / n) of all T. The lengths are read on the
+// device, so the CTAs have equal work whatever the lengths and whatever bound
+// max_l_kv gives. n <= T, so every CTA has a chunk. Called by whole warps.
+struct Work {
+  int64_t total;
+  int n;
+  __device__ __forceinline__ int64_t begin(int i) const { return total * i / n; }
+  // the CTA that has chunk x
+  __device__ __forceinline__ int cta_of(int64_t x) const {
+    return static_cast<int>(((x + 1) * n - 1) / total);
+  }
+};
+
+template <int CH>
+__device__ __forceinline__ int chunks_of(int64_t L) { return static_cast<int>((L + CH - 1) / CH); }
+
+template <int CH>
+__device__ __forceinline__ Work work_of(const Q4Params &p, int lane, bool report) {
+  int64_t t = 0;
+  for (int b = lane; b < p.B; b += 32) t += static_cast<int64_t>(chunks_of<CH>(length(p, b, report))) * p.h_k;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return {t, static_cast<int>(t < p.S ? t : p.S)};
+}
+
+// The sequence that holds chunk x: its first chunk is `start`, each of its rows
+// has nb.
+struct Seq {
+  int64_t start, L;
+  int b, nb;
+};
+
+template <int CH>
+__device__ __forceinline__ Seq seq_at(const Q4Params &p, int lane, int64_t x) {
+  int64_t start = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const int64_t L = b0 + lane < p.B ? length(p, b0 + lane, false) : 0;
+    const int64_t mine = static_cast<int64_t>(chunks_of<CH>(L)) * p.h_k;
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, start + incl > x);
+    if (past != 0u || b0 + 32 >= p.B) {
+      const int at = past != 0u ? __ffs(past) - 1 : 0;
+      Seq s;
+      s.b = b0 + at;
+      s.L = __shfl_sync(0xffffffffu, L, at);
+      s.start = start + __shfl_sync(0xffffffffu, incl - mine, at);
+      s.nb = chunks_of<CH>(s.L);
+      return s;
+    }
+    start += __shfl_sync(0xffffffffu, incl, 31);
+  }
+}
+
+// The pieces of rows in a CTA's chunks [x, end), one after the other.
+struct Piece {
+  int64_t L;
+  int b, kh, c0, c1;            // chunks [c0, c1) of row (b, kh)
+};
+
+template <int CH>
+__device__ __forceinline__ Piece next_piece(const Q4Params &p, Seq &s, int64_t &x, int64_t end) {
+  while (x >= s.start + static_cast<int64_t>(s.nb) * p.h_k) {       // sequences without a chunk fall out
+    s.start += static_cast<int64_t>(s.nb) * p.h_k;
+    s.L = length(p, ++s.b, false);
+    s.nb = chunks_of<CH>(s.L);
+  }
+  const int64_t at = x - s.start;
+  Piece q;
+  q.L = s.L;
+  q.b = s.b;
+  q.kh = static_cast<int>(at / s.nb);
+  q.c0 = static_cast<int>(at % s.nb);
+  const int64_t n = end - x < s.nb - q.c0 ? end - x : s.nb - q.c0;
+  q.c1 = q.c0 + static_cast<int>(n);
+  x += n;
+  return q;
+}
+
+// A CTA's ring of ST stages. Chunk i (counted over all of the CTA's pieces) goes
+// into stage i % ST; kAhead chunks are issued before the first is computed and
+// one more before each, by a lane of warp i % kWarps, so that no warp is slower
+// than the others (a warp of its own for the copies would cost every thread an
+// eighth of its registers). A stage is refilled when the chunk two before the
+// current one has been read by all warps.
+template <int CH, int ST>
+struct Ring {
+  static constexpr int kAhead = ST - 2;
+  static_assert(ST >= 3, "a stage to fill, a stage to read and one between");
+  uint64_t full[ST], empty[ST];
+  int abort;
+
+  __device__ __forceinline__ void init(int warps) {
+    for (int i = 0; i < ST; ++i) {
+      sm100::mbar_init(&full[i], 1);
+      sm100::mbar_init(&empty[i], warps);
+    }
+    abort = 0;
+    sm100::fence_mbar_init();
+  }
+  __device__ __forceinline__ bool gave_up() const { return *reinterpret_cast<const volatile int *>(&abort) != 0; }
+  __device__ __forceinline__ void give_up(int32_t *err) {
+    atomicOr(err, SAGA_DEVERR_TIMEOUT);
+    *reinterpret_cast<volatile int *>(&abort) = 1;
+  }
+  // Issue chunk i, which is `ahead` chunks behind chunk c of piece pc, if the CTA
+  // has it: load(b, kh, L, chunk of the row, stage). (seq, x, end) is the walk
+  // after pc. False when the stage did not become free in time.
+  template <typename F>
+  __device__ __forceinline__ bool issue(const Q4Params &p, int i, const Piece &pc, int c, int ahead, const Seq &seq,
+                                        int64_t x, int64_t end, F load) {
+    const int st = i % ST;
+    if (c + ahead < pc.c1) {
+      if (!wait_bar(&empty[st], ((i / ST) & 1) ^ 1, &abort)) return false;
+      load(pc.b, pc.kh, pc.L, c + ahead, st);
+      return true;
+    }
+    int over = c + ahead - pc.c1;
+    Seq s = seq;
+    while (x < end) {
+      const Piece q = next_piece<CH>(p, s, x, end);
+      if (over < q.c1 - q.c0) {
+        if (!wait_bar(&empty[st], ((i / ST) & 1) ^ 1, &abort)) return false;
+        load(q.b, q.kh, q.L, q.c0 + over, st);
+        return true;
+      }
+      over -= q.c1 - q.c0;
+    }
+    return true;
+  }
+  // After a give-up, before the CTA can exit: the copies of chunks up to i have
+  // landed (a chunk that was never issued ends the wait by its limit).
+  __device__ __forceinline__ void drain(int i) {
+    for (int k = i > ST ? i - ST : 0; k < i; ++k) sm100::mbar_wait(&full[k % ST], (k / ST) & 1);
+  }
+};
 
 }  // namespace q4
 }  // namespace saga

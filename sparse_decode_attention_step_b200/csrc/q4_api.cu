@@ -31,25 +31,11 @@ saga_status check_cache(const saga_q4_cache *c) {
   return SAGA_OK;
 }
 
-// Splits of equal length, a multiple of `chunk`: as many (b, kh, split) units as
-// fit on the GPU at once, for long rows in several waves of at most kMaxSplit
-// positions, so that ragged lengths balance.
-constexpr int64_t kMaxSplit = 16384;
-
-struct Q4Split {
-  int S;
-  int64_t split_len;
-};
-Q4Split split_rows(const saga_shape &s, int64_t chunk, int64_t ctas_per_sm) {
-  const int64_t rows = static_cast<int64_t>(s.B) * s.h_k;
-  const int64_t L = std::max<int64_t>(1, s.max_l_kv);
-  const int64_t slots = kSms * ctas_per_sm;
-  const int64_t waves = std::max<int64_t>(1, ceil_div(rows * L, slots * kMaxSplit));
-  const int64_t target = std::max<int64_t>(1, slots * waves / rows);
-  Q4Split q;
-  q.split_len = ceil_div(ceil_div(L, target), chunk) * chunk;
-  q.S = static_cast<int>(ceil_div(L, q.split_len));
-  return q;
+// CTAs that share the rows: as many as fit on the GPU at once, and no more than
+// there can be chunks.
+int ctas_for(const saga_shape &s, int64_t chunk, int64_t ctas_per_sm) {
+  const int64_t chunks = static_cast<int64_t>(s.B) * s.h_k * std::max<int64_t>(1, ceil_div(s.max_l_kv, chunk));
+  return static_cast<int>(std::min(chunks, kSms * ctas_per_sm));
 }
 
 // Workspace: error and abort words, the records of the dense call or of the
@@ -57,7 +43,7 @@ Q4Split split_rows(const saga_shape &s, int64_t chunk, int64_t ctas_per_sm) {
 // for the refresh the group maxima, their counts and lower bounds.
 struct Q4Plan {
   Plan step;
-  Q4Split dense, scan;
+  int dense, scan;     // CTAs of the dense kernel and of a score pass
   size_t off_records, off_lmask, off_lscore, off_gmax, off_ngroups, off_bound, total;
 };
 Q4Plan q4_plan(const saga_shape &s) {
@@ -65,14 +51,17 @@ Q4Plan q4_plan(const saga_shape &s) {
   saga_shape t = s;
   t.dtype = SAGA_BF16;
   p.step = make_plan(t, true);
-  p.scan = split_rows(s, kQ4ScanChunk, kQ4ScanCtasPerSm);
-  p.dense = {0, 0};
+  p.scan = ctas_for(s, kQ4ScanChunk, kQ4ScanCtasPerSm);
+  p.dense = 0;
   if (dense_supports(s.h_q, s.h_k, s.h_v))
-    p.dense = split_rows(s, q4_dense_chunk(s.h_k, s.h_v), q4_dense_ctas_per_sm(s.d, s.h_q, s.h_k, s.h_v));
+    p.dense = ctas_for(s, q4_dense_chunk(s.d, s.h_q, s.h_k, s.h_v), q4_dense_ctas_per_sm(s.d, s.h_q, s.h_k, s.h_v));
   const size_t rec = static_cast<size_t>(s.d + kRecPad) * sizeof(float);
   const size_t rows = static_cast<size_t>(s.B) * s.h_q, lists = rows * p.step.nblk;
+  // a dense CTA leaves a record for each query head of a row it shares: at most
+  // one row more than there are CTAs between two rows' ends
+  const size_t dense_recs = (p.dense + static_cast<size_t>(s.B) * s.h_k) * (s.h_q / s.h_k);
   p.off_records = kAlign;
-  p.off_lmask = align_up(p.off_records + rows * std::max(p.dense.S, p.step.comb_S) * rec);
+  p.off_lmask = align_up(p.off_records + std::max(dense_recs, rows * p.step.comb_S) * rec);
   p.off_lscore = align_up(p.off_lmask + lists * sizeof(uint32_t));
   p.off_gmax = align_up(p.off_lscore + lists * 32 * sizeof(float));
   p.off_ngroups = align_up(p.off_gmax + lists * 4 * sizeof(float));
@@ -215,13 +204,9 @@ saga_status saga_q4_dense_decode(const saga_shape *shape, const saga_q4_cache *c
   if ((r = check_q4_ws(pl, ws, ws_bytes)) != SAGA_OK) return r;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   Q4Params p = base_params(s, pl, *cache, q, l_kv, ws);
-  p.S = pl.dense.S;
-  p.split_len = pl.dense.split_len;
-  const cudaError_t e = launch_q4_dense(p, s.dtype, s.d, st);
-  if (e != cudaSuccess) return cuda_fail(e, "dense kernel (4-bit)");
-  return cuda_check(launch_combine(p.partials, l_kv, nullptr, out, nullptr, s.B, s.h_q, s.d, p.S,
-                                   p.split_len, s.cap, s.max_l_kv, st),
-                    "combine kernel");
+  p.S = pl.dense;
+  p.out = out;
+  return cuda_check(launch_q4_dense(p, s.dtype, s.d, st), "dense kernel (4-bit)");
 }
 
 saga_status saga_q4_decode_step(const saga_shape *shape, const saga_q4_cache *cache, const void *q,
@@ -237,8 +222,7 @@ saga_status saga_q4_decode_step(const saga_shape *shape, const saga_q4_cache *ca
   if ((r = check_q4_ws(pl, ws, ws_bytes)) != SAGA_OK) return r;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   Q4Params p = base_params(s, pl, *cache, q, l_kv, ws);
-  p.S = pl.scan.S;
-  p.split_len = pl.scan.split_len;
+  p.S = pl.scan;
   p.tau = tau;
   p.sel_mask = sel_mask;
   const cudaError_t e = launch_q4_scan(p, kQ4Step, s.dtype, s.d, st);
@@ -262,8 +246,7 @@ saga_status saga_q4_refresh_threshold(const saga_shape *shape, const saga_q4_cac
   if ((r = check_q4_ws(pl, ws, ws_bytes)) != SAGA_OK) return r;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   Q4Params p = base_params(s, pl, *cache, q, l_kv, ws);
-  p.S = pl.scan.S;
-  p.split_len = pl.scan.split_len;
+  p.S = pl.scan;
   cudaError_t e;
   if (scores != nullptr) {
     p.scores_out = scores;

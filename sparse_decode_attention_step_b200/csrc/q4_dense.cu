@@ -1,12 +1,15 @@
 // Full-attention decode over a 4-bit cache: Eq. (2-4) over every position, for
 // GQA (h_k == h_v) and SAGA heads (VPG = h_v / h_k value heads per key head).
 //
-// One CTA per (b, key head, split of l_kv). A producer warp copies chunks of
-// positions (codes and scales of the key head and its VPG value heads, each a
-// contiguous range) through a ring of shared-memory stages with untiled bulk
-// copies. Eight compute warps each own 32 positions of a chunk (and, with four
-// value heads, two of them) and keep their own running softmax, so they meet
-// only at the ring and at the end. A warp works in registers throughout:
+// As many CTAs as fit on the GPU share the rows (b, key head) in equal runs of
+// chunks, whatever the lengths (see Work in q4.cuh); a row that several CTAs
+// share leaves a record per CTA for the combine kernel below. Chunks of positions
+// (codes and scales of the key head and its VPG value heads, each a contiguous
+// range) come through a ring of shared-memory stages with untiled bulk copies
+// (see Ring). Eight warps each own 32 (or 16) positions of a chunk (and, with four
+// value heads, two of them) and keep their own running softmax,
+// so they meet only at the ring and at the end of a row. A warp works in
+// registers throughout:
 //
 //   scores   S[rows x keys] = Q K^T, mma.sync m16n8k16 with the query rows on M
 //            and eight keys on N: a lane converts the consecutive codes of one
@@ -14,12 +17,16 @@
 //   softmax  per row (a row's scores sit in the four lanes of a quad);
 //   output   O^T[dims x rows] += V^T P^T with the dims on M and the score rows on
 //            N: the scores' accumulators have the layout of the B operand, and
-//            a lane converts the same dims of four keys into the A operand.
+//            a lane converts the same dims of four keys into the A operand. The
+//            operand pairs two keys per register, so the codes of two rows are
+//            interleaved by nibble before they are converted.
 //
 // Probabilities are scaled by 2^7 and split into a high and a low fp16 half
-// (22 bits; fp16 alone would cost the fp32 output its precision), with fp32
-// sums. The running maximum follows the scores lazily: a row is rescaled when
-// its maximum has grown by more than 2^8 of weight, so that P stays below 2^15.
+// (22 bits; fp16 alone would cost the fp32 output its precision). The running
+// maximum follows the scores lazily: a row is rescaled when its maximum has
+// grown by more than 2^8 of weight, so that P stays below 2^15. The tensor cores
+// cut their fp32 sums off instead of rounding them, so a sum runs over a warp's
+// positions of one chunk there and over chunks in rounded fp32 additions.
 //
 // Rows of the score tile (each 8-row tile belongs to one value head):
 //   S    at most 4 query heads per value head: rows 0-3 the heads, rows 4-7 the
@@ -39,11 +46,9 @@ namespace saga {
 
 namespace {
 
-constexpr int kWarps = 8;                       // compute warps; one more produces
-constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kKeysPerWarp = 32;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kPShift = 7.f;                  // P is scaled by 2^kPShift
 constexpr float kLazy = 8.f;                    // log2 growth of a row's maximum that rescales it
 constexpr int kMaxDevices = 64;
@@ -55,116 +60,119 @@ template <int D, int VPW, int MODE, int NG>
 struct QD {
   static constexpr int VPG = VPW * NG;
   static constexpr int SL = kWarps / NG;                        // position slabs of a chunk
-  static constexpr int KC = SL * kKeysPerWarp;
   static constexpr int NRT = MODE == kRowsL16 ? 2 : VPW;        // 8-row score tiles per warp
   static constexpr int MT = (NRT + 1) / 2;                      // 16-row MMA tiles
   static constexpr int NM = D / 16;                             // 16-dim MMA tiles of the output
+  static constexpr int kKeys = D == 128 && NRT == 1 ? 16 : 32;  // positions per warp and chunk (16: room for the ring)
+  static constexpr int NT = kKeys / 8, NJ = kKeys / 16;         // key tiles, 16-key steps
+  static constexpr int KC = SL * kKeys;
   static constexpr int kCodes = KC * D / 2, kScales = KC * D / 16;
   static constexpr int kStage = (kCodes + kScales) * (1 + VPG);
   // two CTAs per SM where the registers allow (the accumulators of a warp are
   // 16 per score tile at d = 64, 32 at d = 128)
   static constexpr int kCtas = NRT * NM <= 8 ? 2 : 1;
-  static constexpr int kBudget = kCtas == 2 ? 108 * 1024 : 200 * 1024;
+  static constexpr int kState = NRT * (NM * 4 + 2);             // a warp's registers to merge
+  static constexpr int kMerge = kWarps / 2 * kState * 32 * 4;
+  static constexpr int kBudget = (kCtas == 2 ? 108 * 1024 : 216 * 1024) - kMerge;
   static constexpr int kStages = kBudget / kStage < 8 ? kBudget / kStage : 8;
-  static constexpr int kRows = NRT * 8;
-  static constexpr int kAccRow = D + 4;                         // floats of a merged row
-  static constexpr int kMerge = kWarps * kRows * kAccRow * 4;
-  static constexpr int kRing = kStages * kStage > kMerge ? kStages * kStage : kMerge;
-  static_assert(kStages >= 2, "a ring");
-  static_assert(kRing <= kBudget + 20 * 1024, "shared memory");
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kSmem = kRing + kMerge;
+  static_assert(kStages >= 3, "a ring");
 };
+
+// Merge a second running softmax state (m2, l2, and acc2 by f(register)) into
+// (m, l, acc) of one row tile: rows g of this lane, columns 2 tq and 2 tq + 1.
+template <int NM, typename F>
+__device__ __forceinline__ void merge_state(float &m, float &l, float (&acc)[NM][4], float m2, float l2, int tq,
+                                            F acc2) {
+  const float mn = fmaxf(m, m2);
+  const float a = m == -INFINITY ? 0.f : q4::ex2(m - mn), c = m2 == -INFINITY ? 0.f : q4::ex2(m2 - mn);
+  m = mn;
+  l = l * a + l2 * c;
+  const float a0 = __shfl_sync(0xffffffffu, a, tq * 8), a1 = __shfl_sync(0xffffffffu, a, tq * 8 + 4);
+  const float c0 = __shfl_sync(0xffffffffu, c, tq * 8), c1 = __shfl_sync(0xffffffffu, c, tq * 8 + 4);
+#pragma unroll
+  for (int n = 0; n < NM; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc[n][e] = acc[n][e] * (e % 2 ? a1 : a0) + acc2(n * 4 + e) * (e % 2 ? c1 : c0);
+}
 
 template <int D, int VPW, int MODE, int NG, typename T>
 __global__ void __launch_bounds__(kThreads, QD<D, VPW, MODE, NG>::kCtas)
 q4_dense_kernel(const Q4Params p) {
   using C = QD<D, VPW, MODE, NG>;
   constexpr bool Q2 = sizeof(T) == 4;
-  constexpr int NRT = C::NRT, MT = C::MT, NM = C::NM, ST = C::kStages;
+  constexpr int NRT = C::NRT, MT = C::MT, NM = C::NM, ST = C::kStages, KC = C::KC, NT = C::NT, NJ = C::NJ;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ uint64_t s_full[ST], s_empty[ST];
-  __shared__ float s_m[kWarps][C::kRows], s_l[kWarps][C::kRows];
-  __shared__ int s_abort;
+  __shared__ q4::Ring<KC, ST> bars;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int s = blockIdx.x;
-  const int b = blockIdx.y / p.h_k, kh = blockIdx.y % p.h_k;
   const int G = p.h_q / p.h_k, HPV = G / C::VPG;
 
-  if (tid == 0) {
-    for (int i = 0; i < ST; ++i) {
-      sm100::mbar_init(&s_full[i], 1);
-      sm100::mbar_init(&s_empty[i], kWarps);
-    }
-    s_abort = 0;
-    sm100::fence_mbar_init();
-  }
+  if (tid == 0) bars.init(kWarps);
   __syncthreads();
   pdl_wait();
   pdl_trigger();
 
-  const int64_t L = q4::length(p, b, tid == 0 && s == 0);
-  const int64_t t_begin = static_cast<int64_t>(s) * p.split_len;
-  if (t_begin >= L) return;
-  const int64_t t_end = min(t_begin + p.split_len, L);
-  const int nchunks = static_cast<int>((t_end - t_begin + C::KC - 1) / C::KC);
+  const int cta = blockIdx.x;
+  const q4::Work work = q4::work_of<KC>(p, lane, cta == 0 && warp == 0);
+  if (cta >= work.n) return;
+  int64_t x0 = work.begin(cta);
+  const int64_t x1 = work.begin(cta + 1);
+  q4::Seq seq = q4::seq_at<KC>(p, lane, x0);
 
-  if (warp == kWarps) {
-    // ---- producer ----------------------------------------------------------
-    if (lane == 0) {
-      const int64_t kb = b * p.kc_sb + kh * p.kc_sh;
-      const int64_t vb = b * p.vc_sb + static_cast<int64_t>(kh) * C::VPG * p.vc_sh;
-      int c = 0;
-      for (; c < nchunks; ++c) {
-        const int st = c % ST;
-        if (!q4::wait_bar(&s_empty[st], ((c / ST) & 1) ^ 1, &s_abort)) break;
-        const int64_t t = t_begin + static_cast<int64_t>(c) * C::KC;
-        // whole groups of four rows: 16 bytes of scales at least (cap is a multiple of 4)
-        const int64_t left = t_end - t;
-        const uint32_t rows = left < C::KC ? static_cast<uint32_t>((left + 3) & ~3ll) : C::KC;
-        const uint32_t nc = rows * (D / 2), ns = rows * (D / 16);
-        uint8_t *dst = ring + st * C::kStage;
-        sm100::mbar_arrive_expect_tx(&s_full[st], (nc + ns) * (1 + C::VPG));
-        q4::bulk_load(dst, p.kc + kb + t * (D / 2), nc, &s_full[st]);
-        uint8_t *dsc = dst + (1 + C::VPG) * C::kCodes;
-        q4::bulk_load(dsc, p.ks + kb / 8 + t * (D / 16), ns, &s_full[st]);
+  const auto load = [&](int b, int kh, int64_t L, int c, int st) {
+    const int64_t kb = b * p.kc_sb + kh * p.kc_sh;
+    const int64_t vb = b * p.vc_sb + static_cast<int64_t>(kh) * C::VPG * p.vc_sh;
+    const int64_t t = static_cast<int64_t>(c) * KC, left = L - t;
+    // whole groups of four rows: 16 bytes of scales at least (cap is a multiple of 4)
+    const uint32_t rows = left < KC ? static_cast<uint32_t>((left + 3) & ~3ll) : KC;
+    const uint32_t nc = rows * (D / 2), ns = rows * (D / 16);
+    uint8_t *dst = ring + st * C::kStage, *dsc = dst + (1 + C::VPG) * C::kCodes;
+    sm100::mbar_arrive_expect_tx(&bars.full[st], (nc + ns) * (1 + C::VPG));
+    q4::bulk_load(dst, p.kc + kb + t * (D / 2), nc, &bars.full[st]);
+    q4::bulk_load(dsc, p.ks + kb / 8 + t * (D / 16), ns, &bars.full[st]);
 #pragma unroll
-        for (int v = 0; v < C::VPG; ++v) {
-          const int64_t vo = vb + v * p.vc_sh;
-          q4::bulk_load(dst + (1 + v) * C::kCodes, p.vc + vo + t * (D / 2), nc, &s_full[st]);
-          q4::bulk_load(dsc + (1 + v) * C::kScales, p.vs + vo / 8 + t * (D / 16), ns, &s_full[st]);
-        }
-      }
-      if (c < nchunks) {
-        atomicOr(p.err, SAGA_DEVERR_TIMEOUT);
-        *reinterpret_cast<volatile int *>(&s_abort) = 1;
-      }
-      // the copies in flight land before the ring is used again
-      for (int i = c > ST ? c - ST : 0; i < c; ++i) sm100::mbar_wait(&s_full[i % ST], (i / ST) & 1);
+    for (int v = 0; v < C::VPG; ++v) {
+      const int64_t vo = vb + v * p.vc_sh;
+      q4::bulk_load(dst + (1 + v) * C::kCodes, p.vc + vo + t * (D / 2), nc, &bars.full[st]);
+      q4::bulk_load(dsc + (1 + v) * C::kScales, p.vs + vo / 8 + t * (D / 16), ns, &bars.full[st]);
     }
-    __syncwarp();
-  }
+  };
+  bool ok = true;
 
   const int g = lane >> 2, tq = lane & 3;
   const int slab = warp / NG, vg = warp % NG;
-  float m[NRT], l[NRT], acc[NRT][NM][4];
-#pragma unroll
-  for (int r = 0; r < NRT; ++r) {
-    m[r] = -INFINITY; l[r] = 0.f;
-#pragma unroll
-    for (int n = 0; n < NM; ++n) acc[r][n][0] = acc[r][n][1] = acc[r][n][2] = acc[r][n][3] = 0.f;
-  }
+  const int key = (g >> 1) + 4 * (g & 1);           // this lane's key of an 8-key tile: column g
+  const int row0 = slab * C::kKeys;
+  float *const merge = reinterpret_cast<float *>(ring + C::kRing);
+  int n_seen = 0;                                    // chunks taken from the ring
 
-  if (warp < kWarps) {
+  while (x0 < x1) {
+    const q4::Piece pc = q4::next_piece<KC>(p, seq, x0, x1);
+    const int b = pc.b, kh = pc.kh;
+    if (n_seen == 0 && tid == 0)
+      for (int i = 0; i < bars.kAhead; ++i) ok = ok && bars.issue(p, i, pc, pc.c0, i, seq, x0, x1, load);
+    __syncwarp();
+    float m[NRT], l[NRT], acc[NRT][NM][4];
+#pragma unroll
+    for (int r = 0; r < NRT; ++r) {
+      m[r] = -INFINITY; l[r] = 0.f;
+#pragma unroll
+      for (int n = 0; n < NM; ++n) acc[r][n][0] = acc[r][n][1] = acc[r][n][2] = acc[r][n][3] = 0.f;
+    }
+
     // ---- query rows ----------------------------------------------------------
     uint32_t qh[MT][D / 16][4], ql[Q2 ? MT : 1][Q2 ? D / 16 : 1][4];
-    float fac[2 * MT];                           // raw score -> log2 units, per row tile
+    float fac[2 * MT];                               // raw score -> log2 units, per row tile
     const float unit = p.scale * kLog2e * kQ4Unit * (p.k_g != nullptr ? __ldg(p.k_g + kh) : 1.f);
     const T *qb = static_cast<const T *>(p.q) + b * p.q_sb;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       // rows g (the even tile) and g + 8 (the odd one)
       const int r0 = 2 * mt, r1 = 2 * mt + 1;
-      const int hd0 = MODE == kRowsS ? (g & 3) : (MODE == kRowsL16 ? g : g);
+      const int hd0 = MODE == kRowsS ? (g & 3) : g;
       const int hd1 = MODE == kRowsS ? (g & 3) : (MODE == kRowsL16 ? 8 + g : g);
       const int v0 = MODE == kRowsL16 ? 0 : vg * VPW + r0, v1 = MODE == kRowsL16 ? 0 : vg * VPW + r1;
       fac[r0] = unit * q4::q_frag<D, T, Q2, 0>(
@@ -184,22 +192,27 @@ q4_dense_kernel(const Q4Params p) {
       }
     }
 
-    const int key = (g >> 1) + 4 * (g & 1);       // this lane's key of an 8-key tile: column g
-    bool ok = true;
-    for (int c = 0; c < nchunks; ++c) {
-      const int st = c % ST;
-      if (!q4::wait_bar(&s_full[st], (c / ST) & 1, &s_abort)) { ok = false; break; }
-      const int row0 = slab * kKeysPerWarp;
-      const int64_t left = t_end - (t_begin + static_cast<int64_t>(c) * C::KC + row0);
+    for (int c = pc.c0; c < pc.c1; ++c, ++n_seen) {
+      const int st = n_seen % ST;
+      // a warp that gave up still meets the others at the barriers below
+      if (warp == n_seen % kWarps && lane == 0)
+        ok = ok && bars.issue(p, n_seen + bars.kAhead, pc, c, bars.kAhead, seq, x0, x1, load);
+      __syncwarp();
+      ok = __all_sync(0xffffffffu, ok && q4::wait_bar(&bars.full[st], (n_seen / ST) & 1, &bars.abort));
+      if (!ok) {
+        if (lane == 0) bars.give_up(p.err);
+        continue;
+      }
+      const int64_t left = pc.L - (static_cast<int64_t>(c) * KC + row0);
       if (left > 0) {
         const uint8_t *codes = ring + st * C::kStage;
         const uint8_t *scales = codes + (1 + C::VPG) * C::kCodes;
         const uint8_t *kc = codes + row0 * (D / 2), *ks = scales + row0 * (D / 16);
 
-        // ---- scores of 32 keys: x[tile][key tile][2 keys of this lane] -------
-        float x[NRT][4][2];
+        // ---- scores of the warp's keys: x[tile][key tile][2 keys of this lane] -------
+        float x[NRT][NT][2];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
+        for (int nt = 0; nt < NT; ++nt) {
           float d[MT][4];
           q4::score_tile<D, MT, Q2>(kc + (8 * nt + key) * (D / 2), ks + (8 * nt + key) * (D / 16), tq,
                                     qh, ql, d);
@@ -209,9 +222,9 @@ q4_dense_kernel(const Q4Params p) {
             x[r][nt][1] = d[r / 2][r % 2 * 2 + 1];
           }
         }
-        if (left < kKeysPerWarp) {                 // columns 2 tq, 2 tq + 1 are keys tq, tq + 4
+        if (left < C::kKeys) {                 // columns 2 tq, 2 tq + 1 are keys tq, tq + 4
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int r = 0; r < NRT; ++r) {
               if (8 * nt + tq >= left) x[r][nt][0] = -INFINITY;
@@ -226,7 +239,7 @@ q4_dense_kernel(const Q4Params p) {
         for (int r = 0; r < NRT; ++r) {
           float mx = fmaxf(x[r][0][0], x[r][0][1]);
 #pragma unroll
-          for (int nt = 1; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(x[r][nt][0], x[r][nt][1]));
+          for (int nt = 1; nt < NT; ++nt) mx = fmaxf(mx, fmaxf(x[r][nt][0], x[r][nt][1]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           cand[r] = mx * fac[r];
@@ -250,12 +263,12 @@ q4_dense_kernel(const Q4Params p) {
         }
 
         // ---- probabilities, as B operands: keys 16 j + .. of row g -------------
-        uint32_t ph[NRT][2][2], pl[MODE == kRowsS ? 1 : NRT][2][2];
+        uint32_t ph[NRT][NJ][2], pl[MODE == kRowsS ? 1 : NRT][NJ][2];
 #pragma unroll
         for (int r = 0; r < NRT; ++r) {
           const float bias = m[r] == -INFINITY ? 0.f : kPShift - m[r];
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt) {
+          for (int nt = 0; nt < NT; ++nt) {
             const float p0 = q4::ex2(fmaf(x[r][nt][0], fac[r], bias));
             const float p1 = q4::ex2(fmaf(x[r][nt][1], fac[r], bias));
             l[r] += p0 + p1;
@@ -270,116 +283,193 @@ q4_dense_kernel(const Q4Params p) {
           }
         }
 
-        // ---- P V: MMA key k of a 16-key step is row tq (2 tq), tq + 4 (2 tq + 1),
-        // tq + 8 (2 tq + 8), tq + 12 (2 tq + 9); this lane's dims: D/8 from g D/8
+        // ---- P V: MMA key k of a 16-key step is row tq (k = 2 tq), tq + 4 (2 tq + 1),
+        // tq + 8 (2 tq + 8), tq + 12 (2 tq + 9); this lane's dims: D/8 from g D/8,
+        // rows g and g + 8 of output tile n its dims 2 n and 2 n + 1
 #pragma unroll
         for (int vw = 0; vw < VPW; ++vw) {
           const int v = vg * VPW + vw;
-          const uint8_t *vc = codes + (1 + v) * C::kCodes + row0 * (D / 2) + g * (D / 16);
-          const uint8_t *vs = scales + (1 + v) * C::kScales + row0 * (D / 16) + (D == 64 ? g / 2 : g);
+          const uint8_t *vc = codes + (1 + v) * C::kCodes + (row0 + tq) * (D / 2) + g * (D / 16);
+          const uint8_t *vs = scales + (1 + v) * C::kScales + (row0 + tq) * (D / 16) + (D == 64 ? g / 2 : g);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t h[4][NM];                     // f16x2 of dims 2 n, 2 n + 1 of key i
+          for (int u = 0; u < D / 64; ++u) {         // eight dims at a time
+            uint32_t a[NJ][4][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = 16 * j + 4 * i + tq;
-              const uint32_t sc = q4::scale_f16(vs[row * (D / 16)]);
-              uint32_t w[D / 64];
-              if constexpr (D == 64) {
-                w[0] = *reinterpret_cast<const uint32_t *>(vc + row * (D / 2));
-              } else {
-                const uint2 y = *reinterpret_cast<const uint2 *>(vc + row * (D / 2));
-                w[0] = y.x; w[1] = y.y;
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+              for (int pr = 0; pr < 2; ++pr) {
+                const int r0 = 16 * j + 8 * pr, r1 = r0 + 4;
+                const uint32_t wa = *reinterpret_cast<const uint32_t *>(vc + r0 * (D / 2) + 4 * u);
+                const uint32_t wb = *reinterpret_cast<const uint32_t *>(vc + r1 * (D / 2) + 4 * u);
+                const uint32_t sc = ((vs[r0 * (D / 16)] + (static_cast<uint32_t>(vs[r1 * (D / 16)]) << 16)) &
+                                     0x007f007fu) * 0x80u;
+                const uint32_t even = (wa & 0x0f0f0f0fu) | ((wb << 4) & 0xf0f0f0f0u);
+                const uint32_t odd = ((wa >> 4) & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u);
+                uint32_t t[4];
+                q4::codes_f16(even, t);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) a[j][n][2 * pr] = q4::mul_f16x2(t[n], sc);
+                q4::codes_f16(odd, t);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) a[j][n][2 * pr + 1] = q4::mul_f16x2(t[n], sc);
               }
 #pragma unroll
-              for (int u = 0; u < D / 64; ++u) {
-                uint32_t t4[4];
-                q4::codes_f16(w[u], t4);
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[i][4 * u + e] = q4::mul_f16x2(t4[e], sc);
-              }
-            }
+              for (int r = 0; r < NRT; ++r) {
+                if (MODE != kRowsL16 && r != vw) continue;
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int n = 0; n < NM; ++n) {
-              const uint32_t a[4] = {__byte_perm(h[0][n], h[1][n], 0x5410), __byte_perm(h[0][n], h[1][n], 0x7632),
-                                     __byte_perm(h[2][n], h[3][n], 0x5410), __byte_perm(h[2][n], h[3][n], 0x7632)};
-              if constexpr (MODE == kRowsL16) {
-#pragma unroll
-                for (int r = 0; r < NRT; ++r) {
-                  q4::mma(acc[r][n], a, ph[r][j][0], ph[r][j][1]);
-                  q4::mma(acc[r][n], a, pl[r][j][0], pl[r][j][1]);
+                for (int j = 0; j < NJ; ++j) {
+                  q4::mma(t, a[j][n], ph[r][j][0], ph[r][j][1]);
+                  if constexpr (MODE != kRowsS) q4::mma(t, a[j][n], pl[r][j][0], pl[r][j][1]);
                 }
-              } else {
-                q4::mma(acc[vw][n], a, ph[vw][j][0], ph[vw][j][1]);
-                if constexpr (MODE == kRowsL8) q4::mma(acc[vw][n], a, pl[vw][j][0], pl[vw][j][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[r][4 * u + n][e] += t[e];
               }
-            }
           }
         }
       }
       __syncwarp();
-      if (lane == 0) sm100::mbar_arrive(&s_empty[st]);
+      if (lane == 0) sm100::mbar_arrive(&bars.empty[st]);
     }
-    if (!ok) {
-      if (lane == 0) atomicOr(p.err, SAGA_DEVERR_TIMEOUT);
-      *reinterpret_cast<volatile int *>(&s_abort) = 1;
-    }
+
+    // ---- the slabs' states, merged pairwise into slab 0 ------------------------
 #pragma unroll
     for (int r = 0; r < NRT; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
     }
-  }
-  __syncthreads();                                  // every copy has landed and been read
+#pragma unroll
+    for (int h = C::SL / 2; h > 0; h /= 2) {
+      sm100::named_bar(1, kWarps * 32);              // the last reads of `merge` are done
+      if (slab >= h && slab < 2 * h) {
+        float *o = merge + ((slab - h) * NG + vg) * (C::kState * 32) + lane;
+#pragma unroll
+        for (int r = 0; r < NRT; ++r) {
+#pragma unroll
+          for (int e = 0; e < NM * 4; ++e) o[(r * (NM * 4 + 2) + e) * 32] = acc[r][e / 4][e % 4];
+          o[(r * (NM * 4 + 2) + NM * 4) * 32] = m[r];
+          o[(r * (NM * 4 + 2) + NM * 4 + 1) * 32] = l[r];
+        }
+      }
+      sm100::named_bar(1, kWarps * 32);
+      if (slab < h) {
+        const float *o = merge + (slab * NG + vg) * (C::kState * 32) + lane;
+#pragma unroll
+        for (int r = 0; r < NRT; ++r) {
+          const float *q = o + r * (NM * 4 + 2) * 32;
+          merge_state<NM>(m[r], l[r], acc[r], q[NM * 4 * 32], q[(NM * 4 + 1) * 32], tq,
+                          [&](int e) { return q[e * 32]; });
+        }
+      }
+    }
+    if (slab != 0) continue;
 
-  // ---- the warps' states, merged in slab order into the heads' records ------
-  float *red = reinterpret_cast<float *>(ring);     // [kWarps][kRows][kAccRow]
-  if (warp < kWarps) {
+    // ---- the heads' outputs, or their records ----------------------------------
+    const bool whole = pc.c0 == 0 && pc.c1 == q4::chunks_of<KC>(pc.L);
+    const bool gave_up = bars.gave_up();
 #pragma unroll
     for (int r = 0; r < NRT; ++r) {
-      if (tq == 0) { s_m[warp][8 * r + g] = m[r]; s_l[warp][8 * r + g] = l[r]; }
-      float *o = red + (warp * C::kRows + 8 * r + 2 * tq) * C::kAccRow + g * (D / 8);
+      const int v = MODE == kRowsL16 ? 0 : vg * VPW + r;
+      const float gv = kQ4Unit * (p.v_g != nullptr ? __ldg(p.v_g + kh * C::VPG + v) : 1.f);
+      if constexpr (MODE == kRowsS) {                // the low halves' sums: rows 4-7
 #pragma unroll
-      for (int n = 0; n < NM; ++n) {
-        o[2 * n] = acc[r][n][0];
-        o[C::kAccRow + 2 * n] = acc[r][n][1];
-        o[2 * n + 1] = acc[r][n][2];
-        o[C::kAccRow + 2 * n + 1] = acc[r][n][3];
+        for (int n = 0; n < NM; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[r][n][e] += __shfl_xor_sync(0xffffffffu, acc[r][n][e], 2);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float mh = __shfl_sync(0xffffffffu, m[r], tq * 8 + 4 * e);
+        const float lh = __shfl_sync(0xffffffffu, l[r], tq * 8 + 4 * e);
+        const int hd = (MODE == kRowsL16 ? 8 * r : 0) + 2 * tq + e;
+        if (hd >= HPV || (MODE == kRowsS && tq >= 2)) continue;
+        const int hg = v * HPV + hd;                 // head of the group
+        float f = gv;
+        float *o;
+        if (whole) {
+          o = p.out + (static_cast<int64_t>(b) * p.h_q + kh * G + hg) * D;
+          f = gave_up ? __int_as_float(0x7fc00000) : gv / lh;
+        } else {
+          o = p.partials + (static_cast<int64_t>(cta + b * p.h_k + kh) * G + hg) * (D + kRecPad);
+          if (g == 0) *reinterpret_cast<float4 *>(o) = make_float4(mh, lh, gave_up ? 1.f : 0.f, 0.f);
+          o += kRecPad;
+        }
+#pragma unroll
+        for (int n = 0; n < NM; ++n)
+          *reinterpret_cast<float2 *>(o + g * (D / 8) + 2 * n) =
+              make_float2(acc[r][n][e] * f, acc[r][n][2 + e] * f);
       }
     }
   }
-  __syncthreads();
-  const bool gave_up = s_abort != 0;
-  for (int idx = tid; idx < G * D; idx += kThreads) {
-    const int hd = idx / D, e = idx % D;            // head of the group, dim
-    const int v = hd / HPV, hv = hd % HPV;
-    const int row = MODE == kRowsL16 ? hv : (v % VPW) * 8 + hv;
-    float M = -INFINITY;
+  if (tid == 0 && !ok) bars.drain(n_seen + ST);
+}
+
+// Rows that several CTAs share: their records {m, l, gave up, -, acc} (m in log2
+// units) merged in CTA order; a row that no CTA had (an empty sequence) becomes
+// zero. One CTA of four warps per (b, query head).
+constexpr int kCombThreads = 128;
+constexpr int kCombWarps = kCombThreads / 32;
+
+template <int D, int CH>
+__global__ void __launch_bounds__(kCombThreads) q4_combine_kernel(const Q4Params p) {
+  constexpr int E = D / 32;
+  __shared__ float s_acc[kCombWarps][D], s_m[kCombWarps], s_l[kCombWarps];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = p.h_q / p.h_k;
+  const int b = blockIdx.x / p.h_q, j = blockIdx.x % p.h_q, kh = j / G;
+  const q4::Work work = q4::work_of<CH>(p, lane, false);
+  int64_t start = 0;                                 // chunks of the sequences before b
+  for (int i = lane; i < b; i += 32) start += static_cast<int64_t>(q4::chunks_of<CH>(q4::length(p, i, false))) * p.h_k;
 #pragma unroll
-    for (int sl = 0; sl < C::SL; ++sl) M = fmaxf(M, s_m[sl * NG + v / VPW][row]);
-    float a = 0.f, ll = 0.f;
-#pragma unroll
-    for (int sl = 0; sl < C::SL; ++sl) {
-      const int w = sl * NG + v / VPW;
-      const float mw = s_m[w][row];
-      const float wt = mw == -INFINITY ? 0.f : q4::ex2(mw - M);
-      const float *o = red + (w * C::kRows + row) * C::kAccRow + e;
-      float x = o[0];
-      if constexpr (MODE == kRowsS) x += o[4 * C::kAccRow];
-      a = fmaf(wt, x, a);
-      ll = fmaf(wt, s_l[w][row], ll);
-    }
-    const int j = kh * G + hd;
-    float *rec = p.partials + (static_cast<int64_t>(b * p.h_q + j) * p.S + s) * (D + kRecPad);
-    const float vg_ = p.v_g != nullptr ? __ldg(p.v_g + kh * C::VPG + v) : 1.f;
-    rec[kRecPad + e] = a * (kQ4Unit * vg_);
-    if (e == 0) {
-      rec[0] = gave_up ? INFINITY : M * kLn2;
-      rec[1] = ll;
-      rec[2] = __int_as_float(gave_up ? -1 : static_cast<int>(t_end - t_begin));
-      rec[3] = 0.f;
-    }
+  for (int o = 16; o > 0; o >>= 1) start += __shfl_xor_sync(0xffffffffu, start, o);
+  const int nb = q4::chunks_of<CH>(q4::length(p, b, false));
+  float *out = p.out + static_cast<int64_t>(blockIdx.x) * D;
+  if (nb == 0) {
+    if (tid < D) out[tid] = 0.f;
+    return;
   }
+  const int64_t x = start + static_cast<int64_t>(kh) * nb;
+  const int i0 = work.cta_of(x), i1 = work.cta_of(x + nb - 1);
+  if (i0 == i1) return;                              // written by that CTA
+
+  float m = -INFINITY, l = 0.f, a[E];
+  bool gave_up = false;
+#pragma unroll
+  for (int e = 0; e < E; ++e) a[e] = 0.f;
+  for (int i = i0 + warp; i <= i1; i += kCombWarps) {
+    const float *r = p.partials + (static_cast<int64_t>(i + b * p.h_k + kh) * G + j % G) * (D + kRecPad);
+    const float4 h = *reinterpret_cast<const float4 *>(r);
+    float v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = r[kRecPad + e * 32 + lane];
+    gave_up |= h.z != 0.f;
+    const float mn = fmaxf(m, h.x);
+    const float ca = m == -INFINITY ? 0.f : q4::ex2(m - mn), cb = h.x == -INFINITY ? 0.f : q4::ex2(h.x - mn);
+    m = mn;
+    l = l * ca + h.y * cb;
+#pragma unroll
+    for (int e = 0; e < E; ++e) a[e] = a[e] * ca + v[e] * cb;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) s_acc[warp][e * 32 + lane] = a[e];
+  if (lane == 0) { s_m[warp] = m; s_l[warp] = gave_up ? __int_as_float(0x7fc00000) : l; }
+  __syncthreads();
+  if (tid >= D) return;
+  float M = s_m[0];
+#pragma unroll
+  for (int w = 1; w < kCombWarps; ++w) M = fmaxf(M, s_m[w]);
+  float o = 0.f, lt = 0.f;
+#pragma unroll
+  for (int w = 0; w < kCombWarps; ++w) {
+    const float c = s_m[w] == -INFINITY ? 0.f : q4::ex2(s_m[w] - M);
+    o = fmaf(c, s_acc[w][tid], o);
+    lt = fmaf(c, s_l[w], lt);
+  }
+  out[tid] = o / lt;
 }
 
 template <int D, int VPW, int MODE, int NG, typename T>
@@ -392,12 +482,13 @@ cudaError_t launch_cfg(const Q4Params &p, cudaStream_t st) {
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(q4_dense_kernel<D, VPW, MODE, NG, T>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kRing);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  return launch_pdl(q4_dense_kernel<D, VPW, MODE, NG, T>, dim3(p.S, p.B * p.h_k), dim3(kThreads), C::kRing,
-                    st, p);
+  e = launch_pdl(q4_dense_kernel<D, VPW, MODE, NG, T>, dim3(p.S), dim3(kThreads), C::kSmem, st, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(q4_combine_kernel<D, C::KC>, dim3(p.B * p.h_q), dim3(kCombThreads), 0, st, p);
 }
 
 // f(cfg) with the configuration of a head layout: S up to 4 query heads per
@@ -423,7 +514,10 @@ struct LaunchQ4 {
 
 }  // namespace
 
-int q4_dense_chunk(int h_k, int h_v) { return h_v / h_k == 4 ? 4 * kKeysPerWarp : 8 * kKeysPerWarp; }
+int q4_dense_chunk(int d, int h_q, int h_k, int h_v) {
+  auto chunk = [](auto c) { return decltype(c)::KC; };
+  return d == 64 ? with_cfg<64>(h_q, h_k, h_v, chunk) : with_cfg<128>(h_q, h_k, h_v, chunk);
+}
 
 int q4_dense_ctas_per_sm(int d, int h_q, int h_k, int h_v) {
   auto ctas = [](auto c) { return decltype(c)::kCtas; };

@@ -34,18 +34,17 @@ struct Q4Read {
 cudaError_t launch_q4_append(const Q4Append &p, int dtype, cudaStream_t st);
 cudaError_t launch_q4_read(const Q4Read &p, int dtype, cudaStream_t st);
 
-// Full attention over grid (S, B * h_k): per-split records for the combine.
-// Head layouts as dense_supports.
+// Full attention by p.S CTAs, then the combine. Head layouts as dense_supports.
 cudaError_t launch_q4_dense(const Q4Params &p, int dtype, int d, cudaStream_t st);
-// The dense kernel's chunk of positions (splits are multiples of it) and CTAs per SM.
-int q4_dense_chunk(int h_k, int h_v);
+// The dense kernel's chunk of positions and CTAs per SM.
+int q4_dense_chunk(int d, int h_q, int h_k, int h_v);
 int q4_dense_ctas_per_sm(int d, int h_q, int h_k, int h_v);
 
-// Score pass over grid (S, B * h_k): the kept lists of p.tau (step), the group
+// Score pass by p.S CTAs: the kept lists of p.tau (step), the group
 // maxima and group counts (max), or the score rows (dump).
 enum { kQ4Step = 0, kQ4Max = 1, kQ4Dump = 2 };
 cudaError_t launch_q4_scan(const Q4Params &p, int mode, int dtype, int d, cudaStream_t st);
-constexpr int kQ4ScanChunk = 256;   // splits are multiples of it
+constexpr int kQ4ScanChunk = 256;
 constexpr int kQ4ScanCtasPerSm = 3;
 
 // tau[b][j] = the N-th largest of row (b, j)'s listed scores, or -inf when

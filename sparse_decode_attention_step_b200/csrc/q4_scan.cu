@@ -16,10 +16,11 @@
 // it, which leaves the step's own kept lists. The K cache is read twice, at 4.5
 // bits a value, where writing and reading the rows would move 8 bytes a score.
 //
-// One CTA per (b, key head, split of l_kv). A producer warp copies chunks of 256
-// positions (codes and scales, two contiguous ranges) through a ring of
-// shared-memory stages with untiled bulk copies; each of eight warps scores
-// its 32 positions: mma.sync m16n8k16 with the heads on M and eight keys on N, a
+// As many CTAs as fit on the GPU share the rows (b, key head) in equal runs of
+// chunks of 256 positions, whatever the lengths (see Work). The chunks (codes
+// and scales, two contiguous ranges) come through a ring of shared-memory stages
+// with untiled bulk copies (see Ring); each of eight warps scores its 32
+// positions: mma.sync m16n8k16 with the heads on M and eight keys on N, a
 // lane converting consecutive codes of one key row into the B operand. A
 // quad of lanes then holds two heads' 32 scores: their masks of kept positions
 // come together in two shuffles, and a kept score goes to its own place in the
@@ -36,7 +37,7 @@ namespace saga {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kThreads = 32 * kWarps;
 constexpr int kChunk = kQ4ScanChunk;
 constexpr int kMaxDevices = 64;
 static_assert(kChunk == kWarps * 32, "a 32-position block per warp");
@@ -45,8 +46,8 @@ template <int D>
 struct QS {
   static constexpr int kCodes = kChunk * D / 2, kScales = kChunk * D / 16;
   static constexpr int kStage = kCodes + kScales;               // 9 KB (d 64), 18 KB
-  static constexpr int kStages = D == 64 ? 6 : 3;
-  static constexpr int kRing = kStages * kStage;                // 54 KB: three CTAs per SM
+  static constexpr int kStages = D == 64 ? 7 : 4;
+  static constexpr int kRing = kStages * kStage;                // 63, 72 KB: three CTAs per SM
 };
 
 template <int D, int MODE, typename T>
@@ -56,90 +57,74 @@ q4_scan_kernel(const Q4Params p) {
   constexpr bool Q2 = sizeof(T) == 4;
   constexpr int ST = C::kStages;
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ uint64_t s_full[ST], s_empty[ST];
-  __shared__ int s_abort;
+  __shared__ q4::Ring<kChunk, ST> bars;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int s = blockIdx.x;
-  const int b = blockIdx.y / p.h_k, kh = blockIdx.y % p.h_k;
   const int G = p.h_q / p.h_k;
 
-  if (tid == 0) {
-    for (int i = 0; i < ST; ++i) {
-      sm100::mbar_init(&s_full[i], 1);
-      sm100::mbar_init(&s_empty[i], kWarps);
-    }
-    s_abort = 0;
-    sm100::fence_mbar_init();
-  }
+  if (tid == 0) bars.init(kWarps);
   __syncthreads();
   pdl_wait();
   pdl_trigger();
 
-  const int64_t L = q4::length(p, b, tid == 0 && s == 0);
-  if (MODE == kQ4Max && s == 0 && kh == 0 && tid == 0) p.n_groups[b] = static_cast<int32_t>((L + 31) / 32 * 4);
-  const int64_t t_begin = static_cast<int64_t>(s) * p.split_len;
-  if (t_begin >= L) return;
-  const int64_t t_end = min(t_begin + p.split_len, L);
-  const int nchunks = static_cast<int>((t_end - t_begin + kChunk - 1) / kChunk);
+  const int cta = blockIdx.x;
+  if (MODE == kQ4Max && cta == 0)
+    for (int b = tid; b < p.B; b += kThreads) p.n_groups[b] = static_cast<int32_t>((q4::length(p, b, false) + 31) / 32 * 4);
+  const q4::Work work = q4::work_of<kChunk>(p, lane, cta == 0 && warp == 0);
+  if (cta >= work.n) return;
+  int64_t x0 = work.begin(cta);
+  const int64_t x1 = work.begin(cta + 1);
+  q4::Seq seq = q4::seq_at<kChunk>(p, lane, x0);
 
-  if (warp == kWarps) {
-    if (lane == 0) {
-      const int64_t kb = b * p.kc_sb + kh * p.kc_sh;
-      int c = 0;
-      for (; c < nchunks; ++c) {
-        const int st = c % ST;
-        if (!q4::wait_bar(&s_empty[st], ((c / ST) & 1) ^ 1, &s_abort)) break;
-        const int64_t t = t_begin + static_cast<int64_t>(c) * kChunk, left = t_end - t;
-        const uint32_t rows = left < kChunk ? static_cast<uint32_t>((left + 3) & ~3ll) : kChunk;
-        const uint32_t nc = rows * (D / 2), ns = rows * (D / 16);
-        uint8_t *dst = ring + st * C::kStage;
-        sm100::mbar_arrive_expect_tx(&s_full[st], nc + ns);
-        q4::bulk_load(dst, p.kc + kb + t * (D / 2), nc, &s_full[st]);
-        q4::bulk_load(dst + C::kCodes, p.ks + kb / 8 + t * (D / 16), ns, &s_full[st]);
-      }
-      if (c < nchunks) {
-        atomicOr(p.err, SAGA_DEVERR_TIMEOUT);
-        atomicExch(p.abort, 1);                    // the gather poisons this step's records
-        *reinterpret_cast<volatile int *>(&s_abort) = 1;
-      }
-      // the copies in flight land before the CTA can exit
-      for (int i = c > ST ? c - ST : 0; i < c; ++i) sm100::mbar_wait(&s_full[i % ST], (i / ST) & 1);
-    }
-    return;
-  }
+  const auto load = [&](int b, int kh, int64_t L, int c, int st) {
+    const int64_t kb = b * p.kc_sb + kh * p.kc_sh;
+    const int64_t t = static_cast<int64_t>(c) * kChunk, left = L - t;
+    // whole groups of four rows: 16 bytes of scales at least (cap is a multiple of 4)
+    const uint32_t rows = left < kChunk ? static_cast<uint32_t>((left + 3) & ~3ll) : kChunk;
+    const uint32_t nc = rows * (D / 2), ns = rows * (D / 16);
+    uint8_t *dst = ring + st * C::kStage;
+    sm100::mbar_arrive_expect_tx(&bars.full[st], nc + ns);
+    q4::bulk_load(dst, p.kc + kb + t * (D / 2), nc, &bars.full[st]);
+    q4::bulk_load(dst + C::kCodes, p.ks + kb / 8 + t * (D / 16), ns, &bars.full[st]);
+  };
+  bool ok = true;
 
   const int g = lane >> 2, tq = lane & 3;
-  const int j0 = kh * G;
+  const bool live[2] = {g < G, g + 8 < G};
+  int n_seen = 0;                                    // chunks taken from the ring
+  while (x0 < x1) {
+  const q4::Piece pc = q4::next_piece<kChunk>(p, seq, x0, x1);
+  const int b = pc.b, j0 = pc.kh * G;
+  if (n_seen == 0 && tid == 0)
+    for (int i = 0; i < bars.kAhead; ++i) ok = ok && bars.issue(p, i, pc, pc.c0, i, seq, x0, x1, load);
+  __syncwarp();
   uint32_t qh[1][D / 16][4], ql[1][Q2 ? D / 16 : 1][4];
   float fac[2], thr[2];
-  const float unit = p.scale * kQ4Unit * (p.k_g != nullptr ? __ldg(p.k_g + kh) : 1.f);
+  const float unit = p.scale * kQ4Unit * (p.k_g != nullptr ? __ldg(p.k_g + pc.kh) : 1.f);
   const T *qb = static_cast<const T *>(p.q) + b * p.q_sb + static_cast<int64_t>(j0 + g) * p.q_sh;
-  fac[0] = unit * q4::q_frag<D, T, Q2, 0>(qb, g < G, tq, qh[0], ql[0]);
-  fac[1] = unit * q4::q_frag<D, T, Q2, 1>(qb + 8 * p.q_sh, g + 8 < G, tq, qh[0], ql[0]);
+  fac[0] = unit * q4::q_frag<D, T, Q2, 0>(qb, live[0], tq, qh[0], ql[0]);
+  fac[1] = unit * q4::q_frag<D, T, Q2, 1>(qb + 8 * p.q_sh, live[1], tq, qh[0], ql[0]);
   if (MODE == kQ4Step) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-      thr[r] = g + 8 * r < G ? p.tau[b * p.h_q + j0 + g + 8 * r] : INFINITY;
+    for (int r = 0; r < 2; ++r) thr[r] = live[r] ? p.tau[b * p.h_q + j0 + g + 8 * r] : INFINITY;
   }
-  // this lane's two heads: the 32-position block t_begin / 32 + warp, moving on
-  // by eight blocks a chunk
-  const int64_t row = static_cast<int64_t>(b) * p.h_q + j0 + g;
-  const int64_t blk0 = t_begin / 32 + warp;
-  const bool live[2] = {g < G, g + 8 < G};
+  const int64_t row = static_cast<int64_t>(b) * p.h_q + j0 + g;     // this lane's first head
 
-  for (int c = 0; c < nchunks; ++c) {
-    const int st = c % ST;
-    if (!q4::wait_bar(&s_full[st], (c / ST) & 1, &s_abort)) {
+  for (int c = pc.c0; c < pc.c1; ++c, ++n_seen) {
+    const int st = n_seen % ST;
+    if (warp == n_seen % kWarps && lane == 0)
+      ok = ok && bars.issue(p, n_seen + bars.kAhead, pc, c, bars.kAhead, seq, x0, x1, load);
+    __syncwarp();
+    if (!__all_sync(0xffffffffu, ok && q4::wait_bar(&bars.full[st], (n_seen / ST) & 1, &bars.abort))) {
       if (lane == 0) {
-        atomicOr(p.err, SAGA_DEVERR_TIMEOUT);
-        atomicExch(p.abort, 1);
+        bars.give_up(p.err);
+        atomicExch(p.abort, 1);                    // the gather poisons this step's records
       }
-      *reinterpret_cast<volatile int *>(&s_abort) = 1;
+      if (tid == 0) bars.drain(n_seen + ST);
       return;
     }
-    const int64_t blk = blk0 + c * kWarps;
-    const int64_t rest = t_end - blk * 32;
+    const int64_t blk = static_cast<int64_t>(c) * kWarps + warp;    // this warp's 32 positions
+    const int64_t rest = pc.L - blk * 32;
     float x[4][4];
     if (rest > 0) {
       const uint8_t *codes = ring + st * C::kStage + (warp * 32 + g) * (D / 2);
@@ -153,7 +138,7 @@ q4_scan_kernel(const Q4Params p) {
       }
     }
     __syncwarp();
-    if (lane == 0) sm100::mbar_arrive(&s_empty[st]);
+    if (lane == 0) sm100::mbar_arrive(&bars.empty[st]);
     if (rest <= 0) continue;
     if (rest < 32 && MODE != kQ4Dump) {            // positions behind the end: below every score
 #pragma unroll
@@ -205,6 +190,7 @@ q4_scan_kernel(const Q4Params p) {
         }
       }
     }
+  }
   }
 }
 
@@ -328,7 +314,7 @@ cudaError_t launch_scan(const Q4Params &p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  return launch_pdl(q4_scan_kernel<D, MODE, T>, dim3(p.S, p.B * p.h_k), dim3(kThreads), QS<D>::kRing, st, p);
+  return launch_pdl(q4_scan_kernel<D, MODE, T>, dim3(p.S), dim3(kThreads), QS<D>::kRing, st, p);
 }
 
 template <int D, typename T>
