@@ -58,9 +58,7 @@ __device__ __forceinline__ bool saga_in_bounds(bool ok, int32_t *err) {
 // cache and the per-split records to write (strides in elements).
 struct GatherParams {
   const uint16_t *V;
-  const uint8_t *vc, *vs;   // a 4-bit cache's codes and scales in place of V (else null)
-  const float *v_g;         // its nullable head scales [h_v]
-  int64_t v_sb, v_sh;       // in elements of V, or bytes of vc (vs has an eighth of them)
+  int64_t v_sb, v_sh;
   const int32_t *l_kv;
   int64_t cap, max_l_kv;
   const uint32_t *lmask;    // [B * h_q][nblk]

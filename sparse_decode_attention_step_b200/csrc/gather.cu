@@ -23,10 +23,6 @@
 // groups and then the warps merge in a fixed order, so the result does not
 // depend on timing, and the CTA writes the head's record.
 //
-// A 4-bit cache (Q4) stages a row as its codes and its scales, D/2 and D/16
-// bytes, and converts them when it folds; the values' common factor goes into
-// the CTA's record. Its scan leaves a kept score at its position in the block.
-//
 // A scan that gave up on a bounded wait sets the step's abort word; this
 // kernel then writes poisoned records (m = +inf, count = -1), which the
 // combine turns into NaN outputs.
@@ -34,7 +30,6 @@
 
 #include "common.cuh"
 #include "kernels.h"
-#include "q4.cuh"
 #include "sm100.cuh"
 
 namespace saga {
@@ -45,7 +40,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D, bool Q4>
+template <int D>
 struct GCfg {
   static constexpr int LPG = D / 8;           // lanes per V row, 16 bytes each
   static constexpr int NG = 32 / LPG;         // lane groups per warp
@@ -55,8 +50,7 @@ struct GCfg {
   // per warp: a 32-block group's list of kept rows (u16 entries), the staged
   // V rows and the staged scores
   static constexpr int kListBytes = 32 * 32 * 2;
-  static constexpr int kRowBytes = Q4 ? D / 2 + 16 : D * 2;   // Q4: codes, then scales
-  static constexpr int kVBytes = kBatch * kRowBytes;
+  static constexpr int kVBytes = kBatch * D * 2;
   static constexpr int kScBytes = kBatch * 4;
   static constexpr int kWarpBytes = kListBytes + kVBytes + kScBytes;
   static constexpr int kMergeBytes = kWarps * kRec * 4;
@@ -71,9 +65,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-template <int D, bool Q4>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 8) gather_kernel(const GatherParams p) {
-  using C = GCfg<D, Q4>;
+  using C = GCfg<D>;
   constexpr int LPG = C::LPG, NG = C::NG, kRows = C::kRows, kBatch = C::kBatch;
   extern __shared__ __align__(16) uint8_t gsm[];
   pdl_wait();
@@ -108,13 +102,10 @@ __global__ void __launch_bounds__(kThreads, 8) gather_kernel(const GatherParams 
 
   const uint32_t *mask = p.lmask + static_cast<int64_t>(bj) * p.nblk;
   const float *sco = p.lscore + static_cast<int64_t>(bj) * p.nblk * 32;
-  // bf16 elements of the head, or its bytes of codes (with 4-bit strides in bytes)
   const uint16_t *vrow = p.V + b * p.v_sb + static_cast<int64_t>(vh) * p.v_sh;
-  const uint8_t *crow = p.vc + b * p.v_sb + static_cast<int64_t>(vh) * p.v_sh;
-  const uint8_t *srow = p.vs + (b * p.v_sb + static_cast<int64_t>(vh) * p.v_sh) / 8;
   uint8_t *wbase = gsm + warp * C::kWarpBytes;
   uint16_t *list = reinterpret_cast<uint16_t *>(wbase);
-  uint8_t *vst = wbase + C::kListBytes;
+  uint16_t *vst = reinterpret_cast<uint16_t *>(wbase + C::kListBytes);
   float *sst = reinterpret_cast<float *>(wbase + C::kListBytes + C::kVBytes);
 
   float m = -INFINITY, l = 0.f, acc[8];
@@ -154,24 +145,9 @@ __global__ void __launch_bounds__(kThreads, 8) gather_kernel(const GatherParams 
       const int i = NG * r + lg;
       if (i < nb) {
         const float pw = ex2((sst[i] - m) * kLog2e);
-        float vf[8];
-        if constexpr (Q4) {
-          const uint8_t *row = vst + i * C::kRowBytes;
-          const uint32_t sc = q4::scale_f16(row[D / 2 + c / 2]);
-          uint32_t h[4];
-          q4::codes_f16(*reinterpret_cast<const uint32_t *>(row + c * 4), h);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t hv = q4::mul_f16x2(h[e], sc);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&hv));
-            vf[2 * e] = f.x;
-            vf[2 * e + 1] = f.y;
-          }
-        } else {
-          const uint4 x = *reinterpret_cast<const uint4 *>(vst + i * C::kRowBytes + c * 16);
-          vf[0] = bf16lo(x.x); vf[1] = bf16hi(x.x); vf[2] = bf16lo(x.y); vf[3] = bf16hi(x.y);
-          vf[4] = bf16lo(x.z); vf[5] = bf16hi(x.z); vf[6] = bf16lo(x.w); vf[7] = bf16hi(x.w);
-        }
+        const uint4 x = *reinterpret_cast<const uint4 *>(vst + i * D + c * 8);
+        const float vf[8] = {bf16lo(x.x), bf16hi(x.x), bf16lo(x.y), bf16hi(x.y),
+                             bf16lo(x.z), bf16hi(x.z), bf16lo(x.w), bf16hi(x.w)};
         l += pw;
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = fmaf(pw, vf[e], acc[e]);
@@ -183,8 +159,6 @@ __global__ void __launch_bounds__(kThreads, 8) gather_kernel(const GatherParams 
   auto run_list = [&](int total, int64_t gb0) {
     // the group's V rows and kept scores, addressed from its first block
     const uint16_t *vg = vrow + gb0 * 32 * D + c * 8;
-    const uint8_t *cg = crow + gb0 * 32 * (D / 2);
-    const uint8_t *xg = srow + gb0 * 32 * (D / 16);
     const float *sg = sco + gb0 * 32;
     for (int pos = 0; pos < total;) {
       const int n = min(kBatch - nst, total - pos);
@@ -198,22 +172,8 @@ __global__ void __launch_bounds__(kThreads, 8) gather_kernel(const GatherParams 
           const uint32_t bl = en >> 10;                        // block within the group
           // a listed row lies inside the sequence and the split
           if (saga_in_bounds(gb0 + bl < blk1 && (gb0 + bl) * 32 + ((en >> 5) & 31) < L, p.err)) {
-            const int t = bl * 32 + ((en >> 5) & 31);
-            if constexpr (Q4) {
-              // D/32 lanes copy the codes, D/64 the scales, the last one the score
-              uint8_t *row = vst + i * C::kRowBytes;
-              if (c < D / 32) {
-                sm100::cp_async16(row + c * 16, cg + t * (D / 2) + c * 16);
-              } else if (c < D / 32 + D / 64) {
-                const int w = c - D / 32;
-                sm100::cp_async4(row + D / 2 + w * 4, xg + t * (D / 16) + w * 4);
-              } else if (c == LPG - 1) {
-                sm100::cp_async4(sst + i, sg + t);       // at its position, not at its rank
-              }
-            } else {
-              sm100::cp_async16(vst + i * C::kRowBytes + c * 16, vg + t * D);
-              if (c == 0) sm100::cp_async4(sst + i, sg + bl * 32 + (en & 31));
-            }
+            sm100::cp_async16(vst + i * D + c * 8, vg + (bl * 32 + ((en >> 5) & 31)) * D);
+            if (c == 0) sm100::cp_async4(sst + i, sg + bl * 32 + (en & 31));
           }
         }
       }
@@ -317,7 +277,6 @@ __global__ void __launch_bounds__(kThreads, 8) gather_kernel(const GatherParams 
       nn += __float_as_int(r[2]);
       aa = fmaf(wt, r[kRecPad + e], aa);
     }
-    if constexpr (Q4) aa *= kQ4Unit * (p.v_g != nullptr ? __ldg(p.v_g + vh) : 1.f);
     rec[kRecPad + e] = aa;
     if (e == 0) {
       rec[0] = mm;
@@ -330,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 8) gather_kernel(const GatherParams 
 
 constexpr int kMaxDevices = 64;
 
-template <int D, bool Q4>
+template <int D>
 cudaError_t launch_d(const GatherParams &p, unsigned grid, cudaStream_t st) {
   static std::atomic<bool> attr_set[kMaxDevices];
   int dev = 0;
@@ -338,12 +297,12 @@ cudaError_t launch_d(const GatherParams &p, unsigned grid, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(gather_kernel<D, Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             GCfg<D, Q4>::kSmem);
+    e = cudaFuncSetAttribute(gather_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             GCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  return launch_pdl(gather_kernel<D, Q4>, dim3(grid), dim3(kThreads), GCfg<D, Q4>::kSmem, st, p);
+  return launch_pdl(gather_kernel<D>, dim3(grid), dim3(kThreads), GCfg<D>::kSmem, st, p);
 }
 
 }  // namespace
@@ -352,14 +311,8 @@ cudaError_t launch_gather(const GatherParams &p, int d, cudaStream_t st) {
   const long long grid = static_cast<long long>(p.B) * p.h_q * p.SB;
   if (grid < 1) return cudaSuccess;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const unsigned n = static_cast<unsigned>(grid);
-  if (p.vc != nullptr) {
-    if (d == 64) return launch_d<64, true>(p, n, st);
-    if (d == 128) return launch_d<128, true>(p, n, st);
-    return cudaErrorInvalidValue;
-  }
-  if (d == 64) return launch_d<64, false>(p, n, st);
-  if (d == 128) return launch_d<128, false>(p, n, st);
+  if (d == 64) return launch_d<64>(p, static_cast<unsigned>(grid), st);
+  if (d == 128) return launch_d<128>(p, static_cast<unsigned>(grid), st);
   return cudaErrorInvalidValue;
 }
 

@@ -28,8 +28,9 @@ struct Q4Params {
   float *partials;             // dense: [S + B * h_k][h_q / h_k][d + kRecPad]
   float *out;                  // dense: [B][h_q][d]
   float *scores_out;           // dump: [B][h_q][row_stride]
-  float *group_max;            // max: [B * h_q][nblk * 4], largest scores of 8-position groups
-  int32_t *n_groups;           // max: [B] groups of each row
+  uint16_t *group_max;         // max: [B * h_q][nblk * 4], largest scores of 8-position groups:
+                               // the upper halves of their order keys
+  int32_t *tickets;            // step: [B * h_q + 1] counters of the gather, cleared here
   uint8_t *sel_mask;           // nullable [B][h_q][row_stride]
   uint32_t *lmask;             // step: [B * h_q][nblk] kept positions of every 32-position block
   float *lscore;               // [B * h_q][nblk * 32] kept scores, each at its position
@@ -72,6 +73,13 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// the same cut off
+__device__ __forceinline__ uint32_t pack_f16_rz(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
 
@@ -151,6 +159,37 @@ __device__ __forceinline__ float q_frag(const T *q, bool live, int tq, uint32_t 
   return __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
 }
 
+// Eight codes of two value rows (keys k and k + 1 of an MMA step) into A operands:
+// register `half` * 2 of tile n holds dim 2 n of both rows, the next one dim 2 n + 1.
+// The rows' codes are interleaved by nibble before they are converted, so that
+// each converted pair holds one dim of both.
+__device__ __forceinline__ void value_pair(uint32_t wa, uint32_t wb, uint32_t sa, uint32_t sb, int half,
+                                           uint32_t (&a)[4][4]) {
+  const uint32_t sc = ((sa + (sb << 16)) & 0x007f007fu) * 0x80u;
+  const uint32_t even = (wa & 0x0f0f0f0fu) | ((wb << 4) & 0xf0f0f0f0u);
+  const uint32_t odd = ((wa >> 4) & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u);
+  uint32_t t[4];
+  codes_f16(even, t);
+#pragma unroll
+  for (int n = 0; n < 4; ++n) a[n][2 * half] = mul_f16x2(t[n], sc);
+  codes_f16(odd, t);
+#pragma unroll
+  for (int n = 0; n < 4; ++n) a[n][2 * half + 1] = mul_f16x2(t[n], sc);
+}
+
+// Where a warp stands in its CTA's ring.
+template <int ST>
+struct Stage {
+  int st = 0;
+  uint32_t phase = 0;          // parity of the stage's current use
+  __device__ __forceinline__ void advance() {
+    if (++st == ST) { st = 0; phase ^= 1u; }
+  }
+  // the stage two before this one, and the parity of its last use's end
+  __device__ __forceinline__ int refill() const { return st >= 2 ? st - 2 : st + ST - 2; }
+  __device__ __forceinline__ uint32_t refill_parity() const { return st >= 2 ? phase : phase ^ 1u; }
+};
+
 // Raw scores (fp16 operands' units) of 16 query rows against eight keys: this
 // lane's key row starts at `codes` and `scales` in shared memory; column c of
 // the tile is the key of the lanes with lane / 4 == c.
@@ -212,9 +251,9 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const i
 
 // A sequence's length in [0, min(cap, max_l_kv)]; a violation is recorded where
 // `report` is set.
-__device__ __forceinline__ int64_t length(const Q4Params &p, int b, bool report) {
-  int64_t L = p.l_kv[b];
-  const int64_t hi = p.cap < p.max_l_kv ? p.cap : p.max_l_kv;
+__device__ __forceinline__ int length(const Q4Params &p, int b, bool report) {
+  int L = p.l_kv[b];
+  const int hi = static_cast<int>(p.cap < p.max_l_kv ? p.cap : p.max_l_kv);   // max_l_kv fits an int
   if (L < 0 || L > hi) {
     if (report) atomicOr(p.err, L < 0 ? SAGA_DEVERR_LKV_NEGATIVE : SAGA_DEVERR_LKV_TOO_LONG);
     L = L < 0 ? 0 : hi;
@@ -238,7 +277,7 @@ struct Work {
 };
 
 template <int CH>
-__device__ __forceinline__ int chunks_of(int64_t L) { return static_cast<int>((L + CH - 1) / CH); }
+__device__ __forceinline__ int chunks_of(int L) { return L / CH + (L % CH != 0); }
 
 template <int CH>
 __device__ __forceinline__ Work work_of(const Q4Params &p, int lane, bool report) {
@@ -252,15 +291,15 @@ __device__ __forceinline__ Work work_of(const Q4Params &p, int lane, bool report
 // The sequence that holds chunk x: its first chunk is `start`, each of its rows
 // has nb.
 struct Seq {
-  int64_t start, L;
-  int b, nb;
+  int64_t start;
+  int b, L, nb;
 };
 
 template <int CH>
 __device__ __forceinline__ Seq seq_at(const Q4Params &p, int lane, int64_t x) {
   int64_t start = 0;
   for (int b0 = 0;; b0 += 32) {
-    const int64_t L = b0 + lane < p.B ? length(p, b0 + lane, false) : 0;
+    const int L = b0 + lane < p.B ? length(p, b0 + lane, false) : 0;
     const int64_t mine = static_cast<int64_t>(chunks_of<CH>(L)) * p.h_k;
     int64_t incl = mine;
 #pragma unroll
@@ -284,8 +323,7 @@ __device__ __forceinline__ Seq seq_at(const Q4Params &p, int lane, int64_t x) {
 
 // The pieces of rows in a CTA's chunks [x, end), one after the other.
 struct Piece {
-  int64_t L;
-  int b, kh, c0, c1;            // chunks [c0, c1) of row (b, kh)
+  int b, kh, L, c0, c1;         // chunks [c0, c1) of row (b, kh)
 };
 
 template <int CH>
@@ -333,35 +371,30 @@ struct Ring {
     atomicOr(err, SAGA_DEVERR_TIMEOUT);
     *reinterpret_cast<volatile int *>(&abort) = 1;
   }
-  // Issue chunk i, which is `ahead` chunks behind chunk c of piece pc, if the CTA
-  // has it: load(b, kh, L, chunk of the row, stage). (seq, x, end) is the walk
-  // after pc. False when the stage did not become free in time.
+  // Issue into stage st, whose last use had `parity`, the chunk that is `ahead`
+  // chunks behind chunk c of piece pc, if the CTA has it: load(b, kh, L, chunk
+  // of the row, stage). (seq, x, end) is the walk after pc. A stage that does not
+  // become free in time is a give-up, which the waits for its chunk see.
   template <typename F>
-  __device__ __forceinline__ bool issue(const Q4Params &p, int i, const Piece &pc, int c, int ahead, const Seq &seq,
-                                        int64_t x, int64_t end, F load) {
-    const int st = i % ST;
-    if (c + ahead < pc.c1) {
-      if (!wait_bar(&empty[st], ((i / ST) & 1) ^ 1, &abort)) return false;
-      load(pc.b, pc.kh, pc.L, c + ahead, st);
-      return true;
+  __device__ __forceinline__ void issue(const Q4Params &p, int st, uint32_t parity, Piece pc, int c, int ahead,
+                                        Seq seq, int64_t x, int64_t end, F load) {
+    c += ahead;
+    while (c >= pc.c1) {
+      if (x >= end) return;
+      c -= pc.c1;
+      pc = next_piece<CH>(p, seq, x, end);
+      c += pc.c0;
     }
-    int over = c + ahead - pc.c1;
-    Seq s = seq;
-    while (x < end) {
-      const Piece q = next_piece<CH>(p, s, x, end);
-      if (over < q.c1 - q.c0) {
-        if (!wait_bar(&empty[st], ((i / ST) & 1) ^ 1, &abort)) return false;
-        load(q.b, q.kh, q.L, q.c0 + over, st);
-        return true;
-      }
-      over -= q.c1 - q.c0;
-    }
-    return true;
+    if (wait_bar(&empty[st], parity, &abort)) load(pc.b, pc.kh, pc.L, c, st);
+    else give_up(p.err);
   }
-  // After a give-up, before the CTA can exit: the copies of chunks up to i have
-  // landed (a chunk that was never issued ends the wait by its limit).
-  __device__ __forceinline__ void drain(int i) {
-    for (int k = i > ST ? i - ST : 0; k < i; ++k) sm100::mbar_wait(&full[k % ST], (k / ST) & 1);
+  // After a give-up, before the CTA can exit: any copies in flight have landed
+  // (the wait for one that was never issued ends by its limit).
+  __device__ __forceinline__ void drain(int st, uint32_t phase) {
+    for (int k = 0; k < ST; ++k) {
+      sm100::mbar_wait(&full[st], phase);
+      if (++st == ST) { st = 0; phase ^= 1u; }
+    }
   }
 };
 

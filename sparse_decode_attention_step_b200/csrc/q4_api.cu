@@ -38,34 +38,43 @@ int ctas_for(const saga_shape &s, int64_t chunk, int64_t ctas_per_sm) {
   return static_cast<int>(std::min(chunks, kSms * ctas_per_sm));
 }
 
+// Splits of a row in the gather: about two waves of CTAs, so that heads that keep
+// more rows than others balance out, each at least kGatherBlocks blocks long.
+constexpr int64_t kGatherCtasPerSm = 16;
+constexpr int64_t kGatherBlocks = 64;
+
 // Workspace: error and abort words, the records of the dense call or of the
-// gather (whose splits are those of the tensor-core step), the kept lists, and
-// for the refresh the group maxima, their counts and lower bounds.
+// gather, the kept lists, the gather's tickets, and for the refresh the group
+// maxima and the lower bounds.
 struct Q4Plan {
-  Plan step;
   int dense, scan;     // CTAs of the dense kernel and of a score pass
-  size_t off_records, off_lmask, off_lscore, off_gmax, off_ngroups, off_bound, total;
+  int SB;              // gather splits of a row
+  int64_t blk_per_split, nblk;
+  size_t off_records, off_lmask, off_lscore, off_tickets, off_gmax, off_bound, total;
 };
 Q4Plan q4_plan(const saga_shape &s) {
   Q4Plan p;
-  saga_shape t = s;
-  t.dtype = SAGA_BF16;
-  p.step = make_plan(t, true);
+  const int64_t items = static_cast<int64_t>(s.B) * s.h_q;
+  p.nblk = std::max<int64_t>(1, ceil_div(s.max_l_kv, 32));
   p.scan = ctas_for(s, kQ4ScanChunk, kQ4ScanCtasPerSm);
+  const int64_t sb = std::min(std::max<int64_t>(1, p.nblk / kGatherBlocks),
+                              std::max<int64_t>(1, kGatherCtasPerSm * kSms / items));
+  p.blk_per_split = ceil_div(p.nblk, sb);
+  p.SB = static_cast<int>(ceil_div(p.nblk, p.blk_per_split));
   p.dense = 0;
   if (dense_supports(s.h_q, s.h_k, s.h_v))
     p.dense = ctas_for(s, q4_dense_chunk(s.d, s.h_q, s.h_k, s.h_v), q4_dense_ctas_per_sm(s.d, s.h_q, s.h_k, s.h_v));
   const size_t rec = static_cast<size_t>(s.d + kRecPad) * sizeof(float);
-  const size_t rows = static_cast<size_t>(s.B) * s.h_q, lists = rows * p.step.nblk;
+  const size_t rows = items, lists = rows * p.nblk;
   // a dense CTA leaves a record for each query head of a row it shares: at most
   // one row more than there are CTAs between two rows' ends
   const size_t dense_recs = (p.dense + static_cast<size_t>(s.B) * s.h_k) * (s.h_q / s.h_k);
   p.off_records = kAlign;
-  p.off_lmask = align_up(p.off_records + std::max(dense_recs, rows * p.step.comb_S) * rec);
+  p.off_lmask = align_up(p.off_records + std::max(dense_recs, rows * p.SB) * rec);
   p.off_lscore = align_up(p.off_lmask + lists * sizeof(uint32_t));
-  p.off_gmax = align_up(p.off_lscore + lists * 32 * sizeof(float));
-  p.off_ngroups = align_up(p.off_gmax + lists * 4 * sizeof(float));
-  p.off_bound = align_up(p.off_ngroups + s.B * sizeof(int32_t));
+  p.off_tickets = align_up(p.off_lscore + lists * 32 * sizeof(float));
+  p.off_gmax = align_up(p.off_tickets + (rows + 1) * sizeof(int32_t));
+  p.off_bound = align_up(p.off_gmax + lists * 4 * sizeof(uint16_t));
   p.total = align_up(p.off_bound + rows * sizeof(float));
   return p;
 }
@@ -98,9 +107,9 @@ Q4Params base_params(const saga_shape &s, const Q4Plan &pl, const saga_q4_cache 
   p.partials = reinterpret_cast<float *>(wsb + pl.off_records);
   p.lmask = reinterpret_cast<uint32_t *>(wsb + pl.off_lmask);
   p.lscore = reinterpret_cast<float *>(wsb + pl.off_lscore);
-  p.group_max = reinterpret_cast<float *>(wsb + pl.off_gmax);
-  p.n_groups = reinterpret_cast<int32_t *>(wsb + pl.off_ngroups);
-  p.nblk = pl.step.nblk;
+  p.group_max = reinterpret_cast<uint16_t *>(wsb + pl.off_gmax);
+  p.tickets = reinterpret_cast<int32_t *>(wsb + pl.off_tickets);
+  p.nblk = pl.nblk;
   p.err = static_cast<int32_t *>(ws);
   p.abort = static_cast<int32_t *>(ws) + 1;
   p.q_sb = s.q_stride_b; p.q_sh = s.q_stride_h;
@@ -112,22 +121,19 @@ Q4Params base_params(const saga_shape &s, const Q4Plan &pl, const saga_q4_cache 
   return p;
 }
 
-// The V half of a step, from the kept lists: gather, then combine.
+// The V half of a step, from the kept lists.
 saga_status run_gather(const saga_shape &s, const Q4Plan &pl, const Q4Params &p, float *out,
                        int32_t *sel_count, cudaStream_t st) {
-  GatherParams g{};
+  Q4Gather g{};
   g.vc = p.vc; g.vs = p.vs; g.v_g = p.v_g;
-  g.v_sb = p.vc_sb; g.v_sh = p.vc_sh;
+  g.vc_sb = p.vc_sb; g.vc_sh = p.vc_sh;
   g.l_kv = p.l_kv; g.cap = p.cap; g.max_l_kv = p.max_l_kv;
   g.lmask = p.lmask; g.lscore = p.lscore; g.nblk = p.nblk;
-  g.partials = p.partials; g.abort = p.abort; g.err = p.err;
-  g.B = s.B; g.h_q = s.h_q; g.SB = pl.step.SB; g.hpv = s.h_q / s.h_v;
-  g.blk_per_split = pl.step.blk_per_split;
-  const cudaError_t e = launch_gather(g, s.d, st);
-  if (e != cudaSuccess) return cuda_fail(e, "gather kernel (4-bit)");
-  return cuda_check(launch_combine(p.partials, p.l_kv, p.abort, out, sel_count, s.B, s.h_q, s.d,
-                                   pl.step.comb_S, pl.step.comb_split_len, s.cap, s.max_l_kv, st),
-                    "combine kernel");
+  g.partials = p.partials; g.out = out; g.sel_count = sel_count;
+  g.tickets = p.tickets; g.abort = p.abort; g.err = p.err;
+  g.B = s.B; g.h_q = s.h_q; g.hpv = s.h_q / s.h_v;
+  g.SB = pl.SB; g.blk_per_split = static_cast<int32_t>(pl.blk_per_split);
+  return cuda_check(launch_q4_gather(g, s.d, st), "gather kernel (4-bit)");
 }
 
 }  // namespace
@@ -258,16 +264,13 @@ saga_status saga_q4_refresh_threshold(const saga_shape *shape, const saga_q4_cac
   if ((e = launch_q4_scan(p, kQ4Max, s.dtype, s.d, st)) != cudaSuccess)
     return cuda_fail(e, "group maximum kernel (4-bit)");
   float *bound = reinterpret_cast<float *>(static_cast<char *>(ws) + pl.off_bound);
-  const int64_t groups = p.nblk * 4;
-  e = launch_radix_select(p.group_max, groups, p.n_groups, N, bound, s.B, s.h_q, groups, groups, nullptr,
-                          nullptr, nullptr, nullptr, nullptr, 0, static_cast<int>(kSms), st);
-  if (e != cudaSuccess) return cuda_fail(e, "radix select kernel");
+  if ((e = launch_q4_bound(p, N, bound, st)) != cudaSuccess) return cuda_fail(e, "bound kernel (4-bit)");
   // 2. the scores that reach it
   p.tau = bound;
   if ((e = launch_q4_scan(p, kQ4Step, s.dtype, s.d, st)) != cudaSuccess)
     return cuda_fail(e, "scan kernel (4-bit)");
   // 3. their N-th largest; for the step, the lists cut down to it
-  if ((e = launch_q4_select(p, N, tau, out != nullptr, sel_mask, st)) != cudaSuccess)
+  if ((e = launch_q4_select(p, N, bound, tau, out != nullptr, sel_mask, st)) != cudaSuccess)
     return cuda_fail(e, "select kernel (4-bit)");
   return out == nullptr ? SAGA_OK : run_gather(s, pl, p, out, sel_count, st);
 }

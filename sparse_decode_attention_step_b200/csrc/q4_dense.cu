@@ -122,12 +122,13 @@ q4_dense_kernel(const Q4Params p) {
   const int64_t x1 = work.begin(cta + 1);
   q4::Seq seq = q4::seq_at<KC>(p, lane, x0);
 
-  const auto load = [&](int b, int kh, int64_t L, int c, int st) {
+  const auto load = [&](int b, int kh, int L, int c, int st) {
     const int64_t kb = b * p.kc_sb + kh * p.kc_sh;
     const int64_t vb = b * p.vc_sb + static_cast<int64_t>(kh) * C::VPG * p.vc_sh;
-    const int64_t t = static_cast<int64_t>(c) * KC, left = L - t;
+    const int64_t t = static_cast<int64_t>(c) * KC;
+    const int left = L - c * KC;
     // whole groups of four rows: 16 bytes of scales at least (cap is a multiple of 4)
-    const uint32_t rows = left < KC ? static_cast<uint32_t>((left + 3) & ~3ll) : KC;
+    const uint32_t rows = left < KC ? (left + 3) & ~3 : KC;
     const uint32_t nc = rows * (D / 2), ns = rows * (D / 16);
     uint8_t *dst = ring + st * C::kStage, *dsc = dst + (1 + C::VPG) * C::kCodes;
     sm100::mbar_arrive_expect_tx(&bars.full[st], (nc + ns) * (1 + C::VPG));
@@ -140,20 +141,22 @@ q4_dense_kernel(const Q4Params p) {
       q4::bulk_load(dsc + (1 + v) * C::kScales, p.vs + vo / 8 + t * (D / 16), ns, &bars.full[st]);
     }
   };
-  bool ok = true;
-
   const int g = lane >> 2, tq = lane & 3;
   const int slab = warp / NG, vg = warp % NG;
   const int key = (g >> 1) + 4 * (g & 1);           // this lane's key of an 8-key tile: column g
   const int row0 = slab * C::kKeys;
+  const float lo_row = g < 4 ? 0.f : -1.f;           // mode S: rows 4-7 take the low halves
   float *const merge = reinterpret_cast<float *>(ring + C::kRing);
-  int n_seen = 0;                                    // chunks taken from the ring
+  q4::Stage<ST> at;
+  int turn = 0;                                      // the warp that issues next
+  bool first = true, ok = true;
 
   while (x0 < x1) {
     const q4::Piece pc = q4::next_piece<KC>(p, seq, x0, x1);
     const int b = pc.b, kh = pc.kh;
-    if (n_seen == 0 && tid == 0)
-      for (int i = 0; i < bars.kAhead; ++i) ok = ok && bars.issue(p, i, pc, pc.c0, i, seq, x0, x1, load);
+    if (first && tid == 0)
+      for (int i = 0; i < bars.kAhead; ++i) bars.issue(p, i, 1u, pc, pc.c0, i, seq, x0, x1, load);
+    first = false;
     __syncwarp();
     float m[NRT], l[NRT], acc[NRT][NM][4];
 #pragma unroll
@@ -192,20 +195,21 @@ q4_dense_kernel(const Q4Params p) {
       }
     }
 
-    for (int c = pc.c0; c < pc.c1; ++c, ++n_seen) {
-      const int st = n_seen % ST;
+    for (int c = pc.c0; c < pc.c1; ++c) {
       // a warp that gave up still meets the others at the barriers below
-      if (warp == n_seen % kWarps && lane == 0)
-        ok = ok && bars.issue(p, n_seen + bars.kAhead, pc, c, bars.kAhead, seq, x0, x1, load);
+      if (!ok) continue;
+      if (warp == turn && lane == 0)
+        bars.issue(p, at.refill(), at.refill_parity(), pc, c, bars.kAhead, seq, x0, x1, load);
+      turn = (turn + 1) % kWarps;
       __syncwarp();
-      ok = __all_sync(0xffffffffu, ok && q4::wait_bar(&bars.full[st], (n_seen / ST) & 1, &bars.abort));
+      ok = __all_sync(0xffffffffu, q4::wait_bar(&bars.full[at.st], at.phase, &bars.abort));
       if (!ok) {
         if (lane == 0) bars.give_up(p.err);
         continue;
       }
-      const int64_t left = pc.L - (static_cast<int64_t>(c) * KC + row0);
+      const int left = pc.L - c * KC - row0;
       if (left > 0) {
-        const uint8_t *codes = ring + st * C::kStage;
+        const uint8_t *codes = ring + at.st * C::kStage;
         const uint8_t *scales = codes + (1 + C::VPG) * C::kCodes;
         const uint8_t *kc = codes + row0 * (D / 2), *ks = scales + row0 * (D / 16);
 
@@ -272,12 +276,13 @@ q4_dense_kernel(const Q4Params p) {
             const float p0 = q4::ex2(fmaf(x[r][nt][0], fac[r], bias));
             const float p1 = q4::ex2(fmaf(x[r][nt][1], fac[r], bias));
             l[r] += p0 + p1;
+            // the high half is p cut off at fp16's 11 bits, the low one the rest
             const float h0 = __uint_as_float(__float_as_uint(p0) & 0xffffe000u);
             const float h1 = __uint_as_float(__float_as_uint(p1) & 0xffffe000u);
             if constexpr (MODE == kRowsS) {
-              ph[r][nt / 2][nt % 2] = q4::pack_f16(g < 4 ? h0 : p0 - h0, g < 4 ? h1 : p1 - h1);
+              ph[r][nt / 2][nt % 2] = q4::pack_f16_rz(fmaf(lo_row, h0, p0), fmaf(lo_row, h1, p1));
             } else {
-              ph[r][nt / 2][nt % 2] = q4::pack_f16(h0, h1);
+              ph[r][nt / 2][nt % 2] = q4::pack_f16_rz(p0, p1);
               pl[r][nt / 2][nt % 2] = q4::pack_f16(p0 - h0, p1 - h1);
             }
           }
@@ -301,17 +306,7 @@ q4_dense_kernel(const Q4Params p) {
                 const int r0 = 16 * j + 8 * pr, r1 = r0 + 4;
                 const uint32_t wa = *reinterpret_cast<const uint32_t *>(vc + r0 * (D / 2) + 4 * u);
                 const uint32_t wb = *reinterpret_cast<const uint32_t *>(vc + r1 * (D / 2) + 4 * u);
-                const uint32_t sc = ((vs[r0 * (D / 16)] + (static_cast<uint32_t>(vs[r1 * (D / 16)]) << 16)) &
-                                     0x007f007fu) * 0x80u;
-                const uint32_t even = (wa & 0x0f0f0f0fu) | ((wb << 4) & 0xf0f0f0f0u);
-                const uint32_t odd = ((wa >> 4) & 0x0f0f0f0fu) | (wb & 0xf0f0f0f0u);
-                uint32_t t[4];
-                q4::codes_f16(even, t);
-#pragma unroll
-                for (int n = 0; n < 4; ++n) a[j][n][2 * pr] = q4::mul_f16x2(t[n], sc);
-                q4::codes_f16(odd, t);
-#pragma unroll
-                for (int n = 0; n < 4; ++n) a[j][n][2 * pr + 1] = q4::mul_f16x2(t[n], sc);
+                q4::value_pair(wa, wb, vs[r0 * (D / 16)], vs[r1 * (D / 16)], pr, a[j]);
               }
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -331,7 +326,8 @@ q4_dense_kernel(const Q4Params p) {
         }
       }
       __syncwarp();
-      if (lane == 0) sm100::mbar_arrive(&bars.empty[st]);
+      if (lane == 0) sm100::mbar_arrive(&bars.empty[at.st]);
+      at.advance();
     }
 
     // ---- the slabs' states, merged pairwise into slab 0 ------------------------
@@ -403,7 +399,7 @@ q4_dense_kernel(const Q4Params p) {
       }
     }
   }
-  if (tid == 0 && !ok) bars.drain(n_seen + ST);
+  if (tid == 0 && !ok) bars.drain(at.st, at.phase);
 }
 
 // Rows that several CTAs share: their records {m, l, gave up, -, acc} (m in log2

@@ -40,16 +40,37 @@ cudaError_t launch_q4_dense(const Q4Params &p, int dtype, int d, cudaStream_t st
 int q4_dense_chunk(int d, int h_q, int h_k, int h_v);
 int q4_dense_ctas_per_sm(int d, int h_q, int h_k, int h_v);
 
-// Score pass by p.S CTAs: the kept lists of p.tau (step), the group
-// maxima and group counts (max), or the score rows (dump).
+// Score pass by p.S CTAs: the kept lists of p.tau (step), the group maxima
+// (max), or the score rows (dump).
 enum { kQ4Step = 0, kQ4Max = 1, kQ4Dump = 2 };
 cudaError_t launch_q4_scan(const Q4Params &p, int mode, int dtype, int d, cudaStream_t st);
 constexpr int kQ4ScanChunk = 256;
-constexpr int kQ4ScanCtasPerSm = 3;
+constexpr int kQ4ScanCtasPerSm = 2;
 
-// tau[b][j] = the N-th largest of row (b, j)'s listed scores, or -inf when
-// N >= l_kv[b]; with `keep`, the lists (and a given sel_mask) are cut down to it.
-cudaError_t launch_q4_select(const Q4Params &p, int32_t N, float *tau, bool keep, uint8_t *sel_mask,
-                             cudaStream_t st);
+// bound[b][j]: a lower bound of the N-th largest score of row (b, j), from the
+// group maxima (-inf with N groups or fewer).
+cudaError_t launch_q4_bound(const Q4Params &p, int32_t N, float *bound, cudaStream_t st);
+
+// tau[b][j] = the N-th largest of row (b, j)'s listed scores, all of them at
+// least bound[b][j], or -inf when N >= l_kv[b]; with `keep`, the lists (and a
+// given sel_mask) are cut down to it.
+cudaError_t launch_q4_select(const Q4Params &p, int32_t N, const float *bound, float *tau, bool keep,
+                             uint8_t *sel_mask, cudaStream_t st);
+
+// The V half of a step from the kept lists, SB CTAs of blk_per_split blocks a row.
+struct Q4Gather {
+  const uint8_t *vc, *vs;
+  const float *v_g;
+  const int32_t *l_kv;
+  const uint32_t *lmask;
+  const float *lscore;
+  float *partials;                 // [B * h_q][SB][d + kRecPad]
+  float *out;
+  int32_t *sel_count;              // nullable
+  int32_t *tickets, *abort, *err;
+  int64_t vc_sb, vc_sh, nblk, cap, max_l_kv;
+  int32_t B, h_q, hpv, SB, blk_per_split;
+};
+cudaError_t launch_q4_gather(const Q4Gather &p, int d, cudaStream_t st);
 
 }  // namespace saga

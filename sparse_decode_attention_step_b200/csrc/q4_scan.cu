@@ -46,13 +46,12 @@ template <int D>
 struct QS {
   static constexpr int kCodes = kChunk * D / 2, kScales = kChunk * D / 16;
   static constexpr int kStage = kCodes + kScales;               // 9 KB (d 64), 18 KB
-  static constexpr int kStages = D == 64 ? 7 : 4;
-  static constexpr int kRing = kStages * kStage;                // 63, 72 KB: three CTAs per SM
+  static constexpr int kStages = D == 64 ? 8 : 5;
+  static constexpr int kRing = kStages * kStage;                // 72, 90 KB: two CTAs per SM
 };
 
 template <int D, int MODE, typename T>
-__global__ void __launch_bounds__(kThreads, D == 128 && sizeof(T) == 4 ? 2 : kQ4ScanCtasPerSm)
-q4_scan_kernel(const Q4Params p) {
+__global__ void __launch_bounds__(kThreads, kQ4ScanCtasPerSm) q4_scan_kernel(const Q4Params p) {
   using C = QS<D>;
   constexpr bool Q2 = sizeof(T) == 4;
   constexpr int ST = C::kStages;
@@ -68,237 +67,377 @@ q4_scan_kernel(const Q4Params p) {
   pdl_trigger();
 
   const int cta = blockIdx.x;
-  if (MODE == kQ4Max && cta == 0)
-    for (int b = tid; b < p.B; b += kThreads) p.n_groups[b] = static_cast<int32_t>((q4::length(p, b, false) + 31) / 32 * 4);
+  if (MODE == kQ4Step && cta == 0)
+    for (int i = tid; i <= p.B * p.h_q; i += kThreads) p.tickets[i] = 0;
   const q4::Work work = q4::work_of<kChunk>(p, lane, cta == 0 && warp == 0);
   if (cta >= work.n) return;
   int64_t x0 = work.begin(cta);
   const int64_t x1 = work.begin(cta + 1);
   q4::Seq seq = q4::seq_at<kChunk>(p, lane, x0);
 
-  const auto load = [&](int b, int kh, int64_t L, int c, int st) {
+  const auto load = [&](int b, int kh, int L, int c, int st) {
     const int64_t kb = b * p.kc_sb + kh * p.kc_sh;
-    const int64_t t = static_cast<int64_t>(c) * kChunk, left = L - t;
+    const int64_t t = static_cast<int64_t>(c) * kChunk;
+    const int left = L - c * kChunk;
     // whole groups of four rows: 16 bytes of scales at least (cap is a multiple of 4)
-    const uint32_t rows = left < kChunk ? static_cast<uint32_t>((left + 3) & ~3ll) : kChunk;
+    const uint32_t rows = left < kChunk ? (left + 3) & ~3 : kChunk;
     const uint32_t nc = rows * (D / 2), ns = rows * (D / 16);
     uint8_t *dst = ring + st * C::kStage;
     sm100::mbar_arrive_expect_tx(&bars.full[st], nc + ns);
     q4::bulk_load(dst, p.kc + kb + t * (D / 2), nc, &bars.full[st]);
     q4::bulk_load(dst + C::kCodes, p.ks + kb / 8 + t * (D / 16), ns, &bars.full[st]);
   };
-  bool ok = true;
 
   const int g = lane >> 2, tq = lane & 3;
   const bool live[2] = {g < G, g + 8 < G};
-  int n_seen = 0;                                    // chunks taken from the ring
+  q4::Stage<ST> at;
+  int turn = 0;                                      // the warp that issues next
+  bool first = true;
   while (x0 < x1) {
-  const q4::Piece pc = q4::next_piece<kChunk>(p, seq, x0, x1);
-  const int b = pc.b, j0 = pc.kh * G;
-  if (n_seen == 0 && tid == 0)
-    for (int i = 0; i < bars.kAhead; ++i) ok = ok && bars.issue(p, i, pc, pc.c0, i, seq, x0, x1, load);
-  __syncwarp();
-  uint32_t qh[1][D / 16][4], ql[1][Q2 ? D / 16 : 1][4];
-  float fac[2], thr[2];
-  const float unit = p.scale * kQ4Unit * (p.k_g != nullptr ? __ldg(p.k_g + pc.kh) : 1.f);
-  const T *qb = static_cast<const T *>(p.q) + b * p.q_sb + static_cast<int64_t>(j0 + g) * p.q_sh;
-  fac[0] = unit * q4::q_frag<D, T, Q2, 0>(qb, live[0], tq, qh[0], ql[0]);
-  fac[1] = unit * q4::q_frag<D, T, Q2, 1>(qb + 8 * p.q_sh, live[1], tq, qh[0], ql[0]);
-  if (MODE == kQ4Step) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) thr[r] = live[r] ? p.tau[b * p.h_q + j0 + g + 8 * r] : INFINITY;
-  }
-  const int64_t row = static_cast<int64_t>(b) * p.h_q + j0 + g;     // this lane's first head
-
-  for (int c = pc.c0; c < pc.c1; ++c, ++n_seen) {
-    const int st = n_seen % ST;
-    if (warp == n_seen % kWarps && lane == 0)
-      ok = ok && bars.issue(p, n_seen + bars.kAhead, pc, c, bars.kAhead, seq, x0, x1, load);
+    const q4::Piece pc = q4::next_piece<kChunk>(p, seq, x0, x1);
+    const int b = pc.b, j0 = pc.kh * G;
+    if (first && tid == 0)
+      for (int i = 0; i < bars.kAhead; ++i) bars.issue(p, i, 1u, pc, pc.c0, i, seq, x0, x1, load);
+    first = false;
     __syncwarp();
-    if (!__all_sync(0xffffffffu, ok && q4::wait_bar(&bars.full[st], (n_seen / ST) & 1, &bars.abort))) {
-      if (lane == 0) {
-        bars.give_up(p.err);
-        atomicExch(p.abort, 1);                    // the gather poisons this step's records
-      }
-      if (tid == 0) bars.drain(n_seen + ST);
-      return;
+    uint32_t qh[1][D / 16][4], ql[1][Q2 ? D / 16 : 1][4];
+    float fac[2], thr[2];
+    const float unit = p.scale * kQ4Unit * (p.k_g != nullptr ? __ldg(p.k_g + pc.kh) : 1.f);
+    const T *qb = static_cast<const T *>(p.q) + b * p.q_sb + static_cast<int64_t>(j0 + g) * p.q_sh;
+    fac[0] = unit * q4::q_frag<D, T, Q2, 0>(qb, live[0], tq, qh[0], ql[0]);
+    fac[1] = unit * q4::q_frag<D, T, Q2, 1>(qb + 8 * p.q_sh, live[1], tq, qh[0], ql[0]);
+    if (MODE == kQ4Step) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) thr[r] = live[r] ? p.tau[b * p.h_q + j0 + g + 8 * r] : INFINITY;
     }
-    const int64_t blk = static_cast<int64_t>(c) * kWarps + warp;    // this warp's 32 positions
-    const int64_t rest = pc.L - blk * 32;
-    float x[4][4];
-    if (rest > 0) {
-      const uint8_t *codes = ring + st * C::kStage + (warp * 32 + g) * (D / 2);
-      const uint8_t *scales = ring + st * C::kStage + C::kCodes + (warp * 32 + g) * (D / 16);
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        float d[1][4];
-        q4::score_tile<D, 1, Q2>(codes + 8 * nt * (D / 2), scales + 8 * nt * (D / 16), tq, qh, ql, d);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[nt][e] = d[0][e];
-      }
-    }
-    __syncwarp();
-    if (lane == 0) sm100::mbar_arrive(&bars.empty[st]);
-    if (rest <= 0) continue;
-    if (rest < 32 && MODE != kQ4Dump) {            // positions behind the end: below every score
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (8 * nt + 2 * tq + (e & 1) >= rest) x[nt][e] = MODE == kQ4Step ? __int_as_float(0x7fc00000) : -INFINITY;
-    }
+    // this lane's places in the outputs of its first head, at 32-position block
+    // 0; the second is eight heads on
+    const int64_t row = static_cast<int64_t>(b) * p.h_q + j0 + g;
+    float *const o_score = MODE == kQ4Step ? p.lscore + row * p.nblk * 32 + 2 * tq : nullptr;
+    float *const o_dump = MODE == kQ4Dump ? p.scores_out + row * p.row_stride + 2 * tq : nullptr;
+    uint16_t *const o_max = MODE == kQ4Max ? p.group_max + row * p.nblk * 4 + tq : nullptr;
+    uint32_t *const o_mask = MODE == kQ4Step ? p.lmask + row * p.nblk : nullptr;
 
+    for (int c = pc.c0; c < pc.c1; ++c) {
+      if (warp == turn && lane == 0)
+        bars.issue(p, at.refill(), at.refill_parity(), pc, c, bars.kAhead, seq, x0, x1, load);
+      turn = (turn + 1) % kWarps;
+      __syncwarp();
+      if (!__all_sync(0xffffffffu, q4::wait_bar(&bars.full[at.st], at.phase, &bars.abort))) {
+        if (lane == 0) {
+          bars.give_up(p.err);
+          atomicExch(p.abort, 1);                  // the gather poisons this step's records
+        }
+        if (tid == 0) bars.drain(at.st, at.phase);
+        return;
+      }
+      const int blk = c * kWarps + warp;           // this warp's 32 positions
+      const int rest = pc.L - blk * 32;
+      float x[4][4];
+      if (rest > 0) {
+        const uint8_t *codes = ring + at.st * C::kStage + (warp * 32 + g) * (D / 2);
+        const uint8_t *scales = ring + at.st * C::kStage + C::kCodes + (warp * 32 + g) * (D / 16);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      if constexpr (MODE == kQ4Max) {
-        float mx = fmaxf(x[0][2 * r], x[0][2 * r + 1]);
+        for (int nt = 0; nt < 4; ++nt) {
+          float d[1][4];
+          q4::score_tile<D, 1, Q2>(codes + 8 * nt * (D / 2), scales + 8 * nt * (D / 16), tq, qh, ql, d);
 #pragma unroll
-        for (int nt = 1; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(x[nt][2 * r], x[nt][2 * r + 1]));
-        if (live[r] && saga_in_bounds(blk < p.nblk, p.err)) p.group_max[((row + 8 * r) * p.nblk + blk) * 4 + tq] = mx * fac[r];
-      } else if constexpr (MODE == kQ4Dump) {
-        float *o = p.scores_out + (row + 8 * r) * p.row_stride + blk * 32;
+          for (int e = 0; e < 4; ++e) x[nt][e] = d[0][e];
+        }
+      }
+      __syncwarp();
+      if (lane == 0) sm100::mbar_arrive(&bars.empty[at.st]);
+      at.advance();
+      if (rest <= 0 || !saga_in_bounds(blk < p.nblk, p.err)) continue;
+      if (rest < 32 && MODE != kQ4Dump) {          // positions behind the end: below every score
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int k = 8 * nt + 2 * tq + e;
-            if (live[r] && k < rest && saga_in_bounds(blk * 32 + k < p.row_stride, p.err)) o[k] = x[nt][2 * r + e] * fac[r];
-          }
-      } else {
-        // NaN behind the end compares false
-        float *o = p.lscore + ((row + 8 * r) * p.nblk + blk) * 32 + 2 * tq;
-        uint32_t mask = 0u;
+          for (int e = 0; e < 4; ++e)
+            if (8 * nt + 2 * tq + (e & 1) >= rest) x[nt][e] = MODE == kQ4Step ? __int_as_float(0x7fc00000) : -INFINITY;
+      }
+
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+      for (int r = 0; r < 2; ++r) {
+        if constexpr (MODE == kQ4Max) {
+          float mx = fmaxf(x[0][2 * r], x[0][2 * r + 1]);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float a = x[nt][2 * r + e] * fac[r];
-            if (a >= thr[r]) {
-              mask |= 1u << (8 * nt + e);
-              o[8 * nt + e] = a;
+          for (int nt = 1; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(x[nt][2 * r], x[nt][2 * r + 1]));
+          if (live[r]) (o_max + 8 * r * p.nblk * 4)[blk * 4] = static_cast<uint16_t>(order_key(mx * fac[r]) >> 16);
+        } else if constexpr (MODE == kQ4Dump) {
+          float *o = o_dump + 8 * r * p.row_stride + static_cast<int64_t>(blk) * 32;
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (live[r] && 8 * nt + 2 * tq + e < rest) o[8 * nt + e] = x[nt][2 * r + e] * fac[r];
+        } else {
+          // NaN behind the end compares false
+          float *o = o_score + 8 * r * p.nblk * 32 + static_cast<int64_t>(blk) * 32;
+          uint32_t mask = 0u;
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float a = x[nt][2 * r + e] * fac[r];
+              if (a >= thr[r]) {
+                mask |= 1u << (8 * nt + e);
+                o[8 * nt + e] = a;
+              }
             }
-          }
-        mask <<= 2 * tq;
-        mask |= __shfl_xor_sync(0xffffffffu, mask, 1);
-        mask |= __shfl_xor_sync(0xffffffffu, mask, 2);
-        if (live[r] && saga_in_bounds(blk < p.nblk, p.err)) {
-          if (tq == 0) p.lmask[(row + 8 * r) * p.nblk + blk] = mask;
-          if (p.sel_mask != nullptr) {
-            uint8_t *sm = p.sel_mask + (row + 8 * r) * p.row_stride + blk * 32;
+          mask <<= 2 * tq;
+          mask |= __shfl_xor_sync(0xffffffffu, mask, 1);
+          mask |= __shfl_xor_sync(0xffffffffu, mask, 2);
+          if (live[r] && tq == 0) (o_mask + 8 * r * p.nblk)[blk] = mask;
+          if (p.sel_mask != nullptr && live[r]) {
+            uint8_t *sm = p.sel_mask + (row + 8 * r) * p.row_stride + static_cast<int64_t>(blk) * 32;
             for (int k = tq; k < 32 && k < rest; k += 4) sm[k] = static_cast<uint8_t>((mask >> k) & 1u);
           }
         }
       }
     }
   }
+}
+
+// The N-th largest of a CTA's keys, given that all lie in [lo, hi] or, if below
+// lo, do not matter, and that N of them reach lo: a histogram of kBins equal
+// ranges of [lo, hi], the range that holds the rank, and again within it, eleven
+// bits at a time. each(f) calls f(key) for every key of the calling thread.
+constexpr int kSelThreads = 512;
+constexpr int kBins = 2048;
+constexpr int kBinsPer = kBins / kSelThreads;
+
+struct Nth {
+  uint32_t hist[kBins], wsum[kSelThreads / 32];
+  uint32_t bin, rem;
+};
+
+template <typename F>
+__device__ __forceinline__ uint32_t nth_largest(uint32_t lo, uint32_t hi, uint32_t N, Nth &sh, F each) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) { sh.bin = 0u; sh.rem = N; }
+  for (;;) {
+    const int shift = hi - lo < kBins ? 0 : 32 - __clz(hi - lo) - 11;
+#pragma unroll
+    for (int e = 0; e < kBinsPer; ++e) sh.hist[tid + e * kSelThreads] = 0u;
+    __syncthreads();
+    each([&](uint32_t k) {
+      if (k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1u);
+    });
+    __syncthreads();
+    // counts from the highest range down; this thread's kBinsPer ranges
+    uint32_t c[kBinsPer], sum = 0u;
+#pragma unroll
+    for (int e = 0; e < kBinsPer; ++e) { c[e] = sh.hist[kBins - 1 - (tid * kBinsPer + e)]; sum += c[e]; }
+    uint32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) sh.wsum[warp] = incl;
+    __syncthreads();
+    uint32_t before = incl - sum;
+    for (int w = 0; w < warp; ++w) before += sh.wsum[w];
+    const uint32_t want = N;
+#pragma unroll
+    for (int e = 0; e < kBinsPer; ++e) {
+      if (before < want && want <= before + c[e]) {
+        sh.bin = kBins - 1 - (tid * kBinsPer + e);
+        sh.rem = want - before;
+      }
+      before += c[e];
+    }
+    __syncthreads();
+    N = sh.rem;
+    lo += sh.bin << shift;
+    if (shift == 0) return lo;
+    const uint32_t top = lo + (1u << shift) - 1u;
+    hi = top < hi ? top : hi;
   }
 }
 
+// The largest of `x` over the CTA, in *s (cleared before).
+__device__ __forceinline__ uint32_t cta_max(uint32_t x, uint32_t *s) {
+  x = __reduce_max_sync(0xffffffffu, x);
+  if ((threadIdx.x & 31) == 0) atomicMax(s, x);
+  __syncthreads();
+  return *s;
+}
+
+// ---- the lower bound from the group maxima ---------------------------------------
+// One CTA per row, the maxima's 16-bit keys in registers (rows beyond 256K
+// positions re-read the rest). Cutting an order key off rounds the score down,
+// so the bound stays one. A row whose rank lies in the sixteen octaves (2048
+// keys) under its maximum takes one histogram.
+constexpr int kBoundRegs = 16;                  // 8-byte words of keys a thread: 32768 keys a CTA
+
+struct BoundParams {
+  const uint16_t *group_max;
+  const int32_t *l_kv;
+  float *bound;
+  int64_t nblk, cap, max_l_kv;
+  int32_t h_q, N;
+};
+
+__global__ void __launch_bounds__(kSelThreads) q4_bound_kernel(const BoundParams p) {
+  __shared__ Nth sh;
+  __shared__ uint32_t s_max, s_near;
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  const int64_t bj = blockIdx.x;
+  int L = p.l_kv[bj / p.h_q];
+  const int cap = static_cast<int>(p.cap < p.max_l_kv ? p.cap : p.max_l_kv);
+  L = L < 0 ? 0 : (L > cap ? cap : L);
+  const int n = (L + 31) / 32 * 4;              // groups of the row
+  if (n < p.N) {
+    if (tid == 0) p.bound[bj] = -INFINITY;
+    return;
+  }
+  if (tid == 0) { s_max = 0u; s_near = 0u; }
+  __syncthreads();
+  // rows start on 8 bytes: four groups a block
+  const uint2 *row = reinterpret_cast<const uint2 *>(p.group_max + bj * p.nblk * 4);
+  const int words = n / 4;
+  uint2 w[kBoundRegs];
+#pragma unroll
+  for (int i = 0; i < kBoundRegs; ++i) {
+    const int at = tid + i * kSelThreads;
+    w[i] = at < words ? row[at] : make_uint2(0u, 0u);   // a key of 0 is below every score's
+  }
+  const auto each = [&](auto f) {
+    const auto four = [&](uint2 x) { f(x.x & 0xffffu); f(x.x >> 16); f(x.y & 0xffffu); f(x.y >> 16); };
+#pragma unroll
+    for (int i = 0; i < kBoundRegs; ++i) {
+      if (i * kSelThreads >= words) break;
+      four(w[i]);
+    }
+    for (int at = tid + kBoundRegs * kSelThreads; at < words; at += kSelThreads) four(row[at]);
+  };
+  uint32_t mx = 0u;
+  each([&](uint32_t k) { mx = max(mx, k); });
+  mx = cta_max(mx, &s_max);
+  const uint32_t near = mx >= kBins ? mx - (kBins - 1) : 1u;
+  uint32_t c = 0u;
+  each([&](uint32_t k) { c += k >= near; });
+  c = __reduce_add_sync(0xffffffffu, c);
+  if ((tid & 31) == 0 && c != 0u) atomicAdd(&s_near, c);
+  __syncthreads();
+  c = s_near;
+  const uint32_t N = static_cast<uint32_t>(p.N);
+  const uint32_t v = c >= N ? nth_largest(near, mx, N, sh, each) : nth_largest(1u, near - 1u, N - c, sh, each);
+  // keys up to that of -inf, cut off, stand for it
+  if (tid == 0) p.bound[bj] = v <= (order_key(-INFINITY) >> 16) ? -INFINITY : from_order_key(v << 16);
+}
+
 // ---- N-th largest of the listed scores ----------------------------------------
-// One CTA per row (b, query head): the listed scores' order keys on chip (in
-// no particular order; they are only counted), then four 8-bit digits from the
-// top, each a histogram and a scan from the highest bin. Lists too long for the
-// chip (ties at the lower bound) are read again for each digit.
-constexpr int kSelThreads = 512;
-constexpr int kSelKeys = 11264;                 // 44 KB
+// One CTA per row (b, query head). The listed positions are gathered on chip
+// first (in no particular order; their scores are only counted), then all their
+// scores at once, then their N-th largest. Lists too long for the chip (ties at
+// the bound, or a large N) are walked again for each histogram.
+constexpr int kSelKeys = 8192;                  // keys and positions: 64 KB
 
 struct SelParams {
   uint32_t *lmask;
-  const float *lscore;
+  const float *lscore, *bound;
   const int32_t *l_kv;
   float *tau;
   uint8_t *sel_mask;             // nullable
   int64_t nblk, cap, max_l_kv;
   int32_t h_q, N;
-  int32_t keep;                  // rewrite the masks with the fresh threshold
+  int32_t keep;                  // cut the masks down to the fresh threshold
 };
 
 __global__ void __launch_bounds__(kSelThreads) q4_select_kernel(const SelParams p) {
-  extern __shared__ uint32_t keys[];            // [kSelKeys]
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t s_n, s_digit, s_rem;
+  extern __shared__ uint32_t keys[];            // [kSelKeys] order keys, [kSelKeys] positions
+  uint32_t *const where = keys + kSelKeys;
+  __shared__ Nth sh;
+  __shared__ uint32_t s_n, s_max;
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int64_t bj = blockIdx.x;
-  const int b = static_cast<int>(bj / p.h_q);
-  int64_t L = p.l_kv[b];
-  const int64_t hi = p.cap < p.max_l_kv ? p.cap : p.max_l_kv;
-  L = L < 0 ? 0 : (L > hi ? hi : L);
-  const int64_t nb = (L + 31) / 32;
+  int L = p.l_kv[bj / p.h_q];
+  const int cap = static_cast<int>(p.cap < p.max_l_kv ? p.cap : p.max_l_kv);
+  L = L < 0 ? 0 : (L > cap ? cap : L);
+  const int nb = (L + 31) / 32;
   uint32_t *mask = p.lmask + bj * p.nblk;
   const float *score = p.lscore + bj * p.nblk * 32;
 
+  uint32_t n = 0u;
   float tau = -INFINITY;
   if (p.N < L) {
-    if (tid == 0) { s_n = 0; s_digit = 0; s_rem = static_cast<uint32_t>(p.N); }
+    const float lo = p.bound[bj];
+    if (tid == 0) { s_n = 0u; s_max = 0u; }
     __syncthreads();
-    for (int64_t i = tid; i < nb; i += kSelThreads) {
-      uint32_t m = mask[i];
-      uint32_t at = m != 0u ? atomicAdd(&s_n, static_cast<uint32_t>(__popc(m))) : 0u;
-      for (; m != 0u; m &= m - 1u, ++at)
-        if (at < kSelKeys) keys[at] = order_key(score[i * 32 + __ffs(m) - 1]);
+    constexpr int U = 8;                        // masks a thread loads at once
+    for (int i0 = 0; i0 < nb; i0 += kSelThreads * U) {
+      uint32_t m[U];
+      int c = 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * kSelThreads + tid;
+        m[u] = i < nb ? mask[i] : 0u;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) c += __popc(m[u]);
+      int incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      uint32_t at = 0u;
+      if (lane == 31 && incl != 0) at = atomicAdd(&s_n, static_cast<uint32_t>(incl));
+      at = __shfl_sync(0xffffffffu, at, 31) + incl - c;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        for (uint32_t x = m[u]; x != 0u; x &= x - 1u, ++at)
+          if (at < kSelKeys) where[at] = (i0 + u * kSelThreads + tid) * 32 + __ffs(x) - 1;
     }
     __syncthreads();
-    const uint32_t n = s_n;
-    uint32_t prefix = 0u, fixed = 0u;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0u;
-      __syncthreads();
-      auto count = [&](uint32_t k) {
-        if ((k & fixed) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
-      };
-      if (n <= kSelKeys) {
-        for (uint32_t i = tid; i < n; i += kSelThreads) count(keys[i]);
+    n = s_n;
+    const bool on_chip = n <= kSelKeys;
+    const auto each = [&](auto f) {             // f(order key)
+      if (on_chip) {
+        for (uint32_t i = tid; i < n; i += kSelThreads) f(keys[i]);
       } else {
-        for (int64_t i = tid; i < nb; i += kSelThreads)
-          for (uint32_t m = mask[i]; m != 0u; m &= m - 1u) count(order_key(score[i * 32 + __ffs(m) - 1]));
+        for (int i = tid; i < nb; i += kSelThreads)
+          for (uint32_t x = mask[i]; x != 0u; x &= x - 1u) f(order_key(score[i * 32 + __ffs(x) - 1]));
       }
-      __syncthreads();
-      // the bin that holds the rank: suffix sums of 256 bins, eight a lane
-      if (warp == 0) {
-        uint32_t c[8], sum = 0u;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) { c[e] = hist[255 - (lane * 8 + e)]; sum += c[e]; }
-        uint32_t incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += y;
-        }
-        uint32_t before = incl - sum;
-        const uint32_t rem = s_rem;
-        __syncwarp();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (before < rem && rem <= before + c[e]) {
-            s_digit = 255u - (lane * 8 + e);
-            s_rem = rem - before;
-          }
-          before += c[e];
-        }
-      }
-      __syncthreads();
-      prefix |= s_digit << shift;
-      fixed |= 255u << shift;
-      __syncthreads();
+    };
+    if (on_chip) {
+#pragma unroll 4
+      for (uint32_t i = tid; i < n; i += kSelThreads) keys[i] = order_key(score[where[i]]);
     }
-    tau = from_order_key(prefix);
+    uint32_t mx = 0u;                           // a thread reads the keys it stored
+    each([&](uint32_t k) { mx = max(mx, k); });
+    mx = cta_max(mx, &s_max);
+    // (-0 and +0 compare equal in the scan: the bound's key is the lower one)
+    tau = from_order_key(nth_largest(order_key(lo == 0.f ? -0.f : lo), mx, static_cast<uint32_t>(p.N), sh, each));
   }
   if (tid == 0) p.tau[bj] = tau;
   if (p.keep == 0) return;
-  for (int64_t i = tid; i < nb; i += kSelThreads) {
-    const uint32_t old = mask[i];
-    uint32_t kept = 0u;
-    for (uint32_t m = old; m != 0u; m &= m - 1u) {
-      const int k = __ffs(m) - 1;
-      if (score[i * 32 + k] >= tau) kept |= 1u << k;
+  if (p.N < L) {
+    const uint32_t k_tau = order_key(tau == 0.f ? -0.f : tau);
+    if (n <= kSelKeys) {
+      for (uint32_t i = tid; i < n; i += kSelThreads)
+        if (keys[i] < k_tau) atomicAnd(&mask[where[i] / 32], ~(1u << (where[i] % 32)));
+    } else {
+      for (int i = tid; i < nb; i += kSelThreads) {
+        uint32_t kept = 0u;
+        for (uint32_t x = mask[i]; x != 0u; x &= x - 1u)
+          if (order_key(score[i * 32 + __ffs(x) - 1]) >= k_tau) kept |= x & (0u - x);
+        mask[i] = kept;
+      }
     }
-    if (kept != old) mask[i] = kept;
-    if (p.sel_mask != nullptr)
-      for (int k = 0; k < 32 && i * 32 + k < L; ++k)
-        p.sel_mask[bj * p.max_l_kv + i * 32 + k] = static_cast<uint8_t>((kept >> k) & 1u);
   }
+  if (p.sel_mask == nullptr) return;
+  __threadfence();
+  __syncthreads();
+  for (int t = tid; t < L; t += kSelThreads)
+    p.sel_mask[bj * p.max_l_kv + t] = static_cast<uint8_t>((*reinterpret_cast<volatile uint32_t *>(mask + t / 32) >> (t % 32)) & 1u);
 }
 
 template <int D, int MODE, typename T>
@@ -336,11 +475,27 @@ cudaError_t launch_q4_scan(const Q4Params &p, int mode, int dtype, int d, cudaSt
   return d == 64 ? launch_scan_m<64, float>(p, mode, st) : launch_scan_m<128, float>(p, mode, st);
 }
 
-cudaError_t launch_q4_select(const Q4Params &p, int32_t N, float *tau, bool keep, uint8_t *sel_mask,
-                             cudaStream_t st) {
-  static_assert(kSelKeys * 4 + 2048 <= 48 * 1024, "no opt-in shared memory");
-  const SelParams sp{p.lmask, p.lscore, p.l_kv, tau, sel_mask, p.nblk, p.cap, p.max_l_kv, p.h_q, N, keep ? 1 : 0};
-  return launch_pdl(q4_select_kernel, dim3(p.B * p.h_q), dim3(kSelThreads), kSelKeys * 4, st, sp);
+cudaError_t launch_q4_bound(const Q4Params &p, int32_t N, float *bound, cudaStream_t st) {
+  const BoundParams bp{p.group_max, p.l_kv, bound, p.nblk, p.cap, p.max_l_kv, p.h_q, N};
+  return launch_pdl(q4_bound_kernel, dim3(p.B * p.h_q), dim3(kSelThreads), 0, st, bp);
+}
+
+cudaError_t launch_q4_select(const Q4Params &p, int32_t N, const float *bound, float *tau, bool keep,
+                             uint8_t *sel_mask, cudaStream_t st) {
+  static std::atomic<bool> attr_set[kMaxDevices];
+  constexpr int kSmem = 2 * kSelKeys * 4;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (!attr_set[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(q4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    attr_set[dev].store(true, std::memory_order_release);
+  }
+  const SelParams sp{p.lmask, p.lscore, bound, p.l_kv, tau, sel_mask, p.nblk, p.cap, p.max_l_kv, p.h_q, N,
+                     keep ? 1 : 0};
+  return launch_pdl(q4_select_kernel, dim3(p.B * p.h_q), dim3(kSelThreads), kSmem, st, sp);
 }
 
 }  // namespace saga
