@@ -38,10 +38,10 @@ int ctas_for(const saga_shape &s, int64_t chunk, int64_t ctas_per_sm) {
   return static_cast<int>(std::min(chunks, kSms * ctas_per_sm));
 }
 
-// Splits of a row in the gather: about two waves of CTAs, so that heads that keep
-// more rows than others balance out, each at least kGatherBlocks blocks long.
-constexpr int64_t kGatherCtasPerSm = 16;
-constexpr int64_t kGatherBlocks = 64;
+// CTAs of the gather in all, and the blocks of a row that each has at least: few
+// enough that a warp has several batches of rows to overlap.
+constexpr int64_t kGatherCtasPerSm = 4;
+constexpr int64_t kGatherBlocks = 128;
 
 // Workspace: error and abort words, the records of the dense call or of the
 // gather, the kept lists, the gather's tickets, and for the refresh the group

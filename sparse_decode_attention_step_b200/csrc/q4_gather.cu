@@ -40,7 +40,7 @@ struct Rows {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 6 : 4) q4_gather_kernel(const Q4Gather p) {
+__global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) q4_gather_kernel(const Q4Gather p) {
   constexpr int NM = D / 16;
   __shared__ int list[kWarps][32 * 32 + kBatch];
   __shared__ float s_acc[kWarps][D], s_m[kWarps], s_l[kWarps];
@@ -69,15 +69,16 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 6 : 4) q4_gather_kernel(co
   for (int n = 0; n < NM; ++n) acc[n][0] = acc[n][1] = 0.f;
   int kept = 0;
 
-  // entries [at, at + n) of the list, n <= kBatch; entries behind them count nothing
-  auto load = [&](int at, int n, Rows<D> &r) {
+  // n <= kBatch positions of the list, from at_list on; the others of a batch count nothing
+  int at_list = 0;
+  auto load = [&](int n, Rows<D> &r) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int e = 16 * j + tq + 4 * i;
         const bool in = e < n;
-        const int64_t pos = mine[at + (in ? e : 0)];
+        const int64_t pos = mine[at_list + (in ? e : 0)];
         const uint8_t *c = codes + pos * (D / 2);
         if constexpr (D == 64) {
           r.code[j][i][0] = __ldg(reinterpret_cast<const uint32_t *>(c));
@@ -141,54 +142,56 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 6 : 4) q4_gather_kernel(co
   if (!gave_up) {
     const int per = (blk1 - blk0 + kWarps - 1) / kWarps;
     const int w0 = min(blk0 + per * warp, blk1), w1 = min(w0 + per, blk1);
-    Rows<D> r0, r1;                              // one is worked on while the other's loads are under way
-    int have = 0;                                // entries on the list
-    int held = 0;                                // 1: r0 holds loaded rows, 2: r1 does
-    const auto step = [&](int at, int n) {
-      if (held == 1) {
-        load(at, n, r1);
-        fold(r0);
-        held = 2;
-      } else {
-        load(at, n, r0);
-        if (held == 2) fold(r1);
-        held = 1;
-      }
-    };
-    // blocks' masks are read 32 at a time, the next ones ahead of their use
+    // The next batch onto the list: its positions, 0 when there are none left. The
+    // blocks' masks are taken 32 at a time, read ahead of their use.
+    int wb = w0, have = 0, used = 0;
     uint32_t next = w0 + lane < w1 ? mask[w0 + lane] : 0u;
-    for (int wb = w0; wb < w1; wb += 32) {
-      uint32_t mk = next;
-      next = wb + 32 + lane < w1 ? mask[wb + 32 + lane] : 0u;
-      const int cn = __popc(mk);
-      int incl = cn;
+    const auto next_batch = [&]() {
+      have -= used;                              // what the last batches left moves to the front
+      at_list += used;
+      if (have < kBatch && at_list > 0) {
+        const int v = mine[at_list + (lane < have ? lane : 0)];
+        __syncwarp();
+        if (lane < have) mine[lane] = v;
+        at_list = 0;
+      }
+      while (have < kBatch && wb < w1) {
+        uint32_t mk = next;
+        next = wb + 32 + lane < w1 ? mask[wb + 32 + lane] : 0u;
+        const int cn = __popc(mk);
+        int incl = cn;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        for (int e = have + incl - cn; mk != 0u; mk &= mk - 1u, ++e) {
+          const int pos = (wb + lane) * 32 + __ffs(mk) - 1;
+          mine[e] = saga_in_bounds(pos < L, p.err) ? pos : 0;
+        }
+        const int total = __shfl_sync(0xffffffffu, incl, 31);
+        have += total;
+        kept += total;
+        wb += 32;
       }
-      const int total = __shfl_sync(0xffffffffu, incl, 31);
-      if (total == 0) continue;
-      kept += total;
-      for (int e = have + incl - cn; mk != 0u; mk &= mk - 1u, ++e) {
-        const int pos = (wb + lane) * 32 + __ffs(mk) - 1;
-        mine[e] = saga_in_bounds(pos < L, p.err) ? pos : 0;
+      __syncwarp();
+      used = min(have, kBatch);
+      return used;
+    };
+    // one batch is worked on while the next one's loads are under way
+    Rows<D> r0, r1;
+    int n = next_batch();
+    if (n > 0) {
+      load(n, r0);
+      for (;;) {
+        if ((n = next_batch()) == 0) { fold(r0); break; }
+        load(n, r1);
+        fold(r0);
+        if ((n = next_batch()) == 0) { fold(r1); break; }
+        load(n, r0);
+        fold(r1);
       }
-      have += total;
-      __syncwarp();
-      int at = 0;
-      for (; have - at >= kBatch; at += kBatch) step(at, kBatch);
-      // the rest moves to the front
-      const int rest = have - at;
-      const int v = lane < rest ? mine[at + lane] : 0;
-      __syncwarp();
-      if (lane < rest) mine[lane] = v;
-      have = rest;
-      __syncwarp();
     }
-    if (have > 0) step(0, have);
-    if (held == 1) fold(r0);
-    if (held == 2) fold(r1);
   }
 
   // ---- the warps' states, then the CTA's record -------------------------------

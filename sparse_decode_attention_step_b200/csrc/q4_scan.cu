@@ -173,21 +173,22 @@ __global__ void __launch_bounds__(kThreads, kQ4ScanCtasPerSm) q4_scan_kernel(con
               if (live[r] && 8 * nt + 2 * tq + e < rest) o[8 * nt + e] = x[nt][2 * r + e] * fac[r];
         } else {
           // NaN behind the end compares false
-          float *o = o_score + 8 * r * p.nblk * 32 + static_cast<int64_t>(blk) * 32;
+          float a[8];
           uint32_t mask = 0u;
 #pragma unroll
-          for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float a = x[nt][2 * r + e] * fac[r];
-              if (a >= thr[r]) {
-                mask |= 1u << (8 * nt + e);
-                o[8 * nt + e] = a;
-              }
-            }
+          for (int i = 0; i < 8; ++i) {
+            a[i] = x[i / 2][2 * r + i % 2] * fac[r];
+            if (a[i] >= thr[r]) mask |= 1u << (8 * (i / 2) + i % 2);
+          }
           mask <<= 2 * tq;
           mask |= __shfl_xor_sync(0xffffffffu, mask, 1);
           mask |= __shfl_xor_sync(0xffffffffu, mask, 2);
+          // a quad's eight scores of a key tile are one sector: written whole when
+          // one of them is kept, so that reading it back needs no fill from memory
+          float2 *o = reinterpret_cast<float2 *>(o_score + 8 * r * p.nblk * 32 + static_cast<int64_t>(blk) * 32);
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt)
+            if (mask & (0xffu << (8 * nt))) o[4 * nt] = make_float2(a[2 * nt], a[2 * nt + 1]);
           if (live[r] && tq == 0) (o_mask + 8 * r * p.nblk)[blk] = mask;
           if (p.sel_mask != nullptr && live[r]) {
             uint8_t *sm = p.sel_mask + (row + 8 * r) * p.row_stride + static_cast<int64_t>(blk) * 32;
