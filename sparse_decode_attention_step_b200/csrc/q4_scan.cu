@@ -202,10 +202,10 @@ __global__ void __launch_bounds__(kThreads, kQ4ScanCtasPerSm) q4_scan_kernel(con
 
 // The N-th largest of a CTA's keys, given that all lie in [lo, hi] or, if below
 // lo, do not matter, and that N of them reach lo: a histogram of kBins equal
-// ranges of [lo, hi], the range that holds the rank, and again within it, eleven
+// ranges of [lo, hi], the range that holds the rank, and again within it, ten
 // bits at a time. each(f) calls f(key) for every key of the calling thread.
 constexpr int kSelThreads = 512;
-constexpr int kBins = 2048;
+constexpr int kBins = 1024;
 constexpr int kBinsPer = kBins / kSelThreads;
 
 struct Nth {
@@ -218,7 +218,7 @@ __device__ __forceinline__ uint32_t nth_largest(uint32_t lo, uint32_t hi, uint32
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) { sh.bin = 0u; sh.rem = N; }
   for (;;) {
-    const int shift = hi - lo < kBins ? 0 : 32 - __clz(hi - lo) - 11;
+    const int shift = hi - lo < kBins ? 0 : 32 - __clz(hi - lo) - 10;
 #pragma unroll
     for (int e = 0; e < kBinsPer; ++e) sh.hist[tid + e * kSelThreads] = 0u;
     __syncthreads();
@@ -267,11 +267,11 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t x, uint32_t *s) {
 }
 
 // ---- the lower bound from the group maxima ---------------------------------------
-// One CTA per row, the maxima's 16-bit keys in registers (rows beyond 256K
+// One CTA per row, the maxima's 16-bit keys in registers (rows beyond 128K
 // positions re-read the rest). Cutting an order key off rounds the score down,
-// so the bound stays one. A row whose rank lies in the sixteen octaves (2048
+// so the bound stays one. A row whose rank lies in the eight octaves (1024
 // keys) under its maximum takes one histogram.
-constexpr int kBoundRegs = 16;                  // 8-byte words of keys a thread: 32768 keys a CTA
+constexpr int kBoundRegs = 8;                   // 8-byte words of keys a thread: 16384 keys a CTA
 
 struct BoundParams {
   const uint16_t *group_max;
@@ -281,7 +281,7 @@ struct BoundParams {
   int32_t h_q, N;
 };
 
-__global__ void __launch_bounds__(kSelThreads) q4_bound_kernel(const BoundParams p) {
+__global__ void __launch_bounds__(kSelThreads, 3) q4_bound_kernel(const BoundParams p) {
   __shared__ Nth sh;
   __shared__ uint32_t s_max, s_near;
   pdl_wait();
@@ -333,11 +333,13 @@ __global__ void __launch_bounds__(kSelThreads) q4_bound_kernel(const BoundParams
 }
 
 // ---- N-th largest of the listed scores ----------------------------------------
-// One CTA per row (b, query head). The listed positions are gathered on chip
-// first (in no particular order; their scores are only counted), then all their
-// scores at once, then their N-th largest. Lists too long for the chip (ties at
-// the bound, or a large N) are walked again for each histogram.
-constexpr int kSelKeys = 8192;                  // keys and positions: 64 KB
+// One CTA per row (b, query head). The listed scores are gathered on chip (in no
+// particular order; they are only counted), then their N-th largest. A sparse
+// list's positions are gathered first, a thread per 32-position block, then all
+// its scores at once; a dense one (a short row, where N groups are most of it)
+// is read a block per warp. Lists too long for the chip (ties at the bound, or a
+// large N) are read that way again for each histogram.
+constexpr int kSelWords = 10240;                // keys, or half as many keys and positions: 40 KB, four CTAs per SM
 
 struct SelParams {
   uint32_t *lmask;
@@ -350,14 +352,14 @@ struct SelParams {
   int32_t keep;                  // cut the masks down to the fresh threshold
 };
 
-__global__ void __launch_bounds__(kSelThreads) q4_select_kernel(const SelParams p) {
-  extern __shared__ uint32_t keys[];            // [kSelKeys] order keys, [kSelKeys] positions
-  uint32_t *const where = keys + kSelKeys;
+__global__ void __launch_bounds__(kSelThreads, 4) q4_select_kernel(const SelParams p) {
+  extern __shared__ uint32_t keys[];            // [kSelWords]
+  uint32_t *const where = keys + kSelWords / 2;
   __shared__ Nth sh;
-  __shared__ uint32_t s_n, s_max;
+  __shared__ uint32_t s_n, s_at, s_max;
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t bj = blockIdx.x;
   int L = p.l_kv[bj / p.h_q];
   const int cap = static_cast<int>(p.cap < p.max_l_kv ? p.cap : p.max_l_kv);
@@ -365,17 +367,26 @@ __global__ void __launch_bounds__(kSelThreads) q4_select_kernel(const SelParams 
   const int nb = (L + 31) / 32;
   uint32_t *mask = p.lmask + bj * p.nblk;
   const float *score = p.lscore + bj * p.nblk * 32;
+  // f(block, mask, this lane's score) for the blocks of this warp, which all lanes call
+  const auto walk = [&](auto f) {
+#pragma unroll 4
+    for (int i = warp; i < nb; i += kSelThreads / 32) {
+      const uint32_t m = mask[i];
+      f(i, m, (m >> lane) & 1u ? score[i * 32 + lane] : 0.f);
+    }
+  };
 
-  uint32_t n = 0u;
   float tau = -INFINITY;
+  bool sparse = false;
+  uint32_t n = 0u;
   if (p.N < L) {
     const float lo = p.bound[bj];
-    if (tid == 0) { s_n = 0u; s_max = 0u; }
+    if (tid == 0) { s_n = 0u; s_at = 0u; s_max = 0u; }
     __syncthreads();
     constexpr int U = 8;                        // masks a thread loads at once
+    uint32_t m[U];
+    uint32_t c = 0u;
     for (int i0 = 0; i0 < nb; i0 += kSelThreads * U) {
-      uint32_t m[U];
-      int c = 0;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = i0 + u * kSelThreads + tid;
@@ -383,36 +394,56 @@ __global__ void __launch_bounds__(kSelThreads) q4_select_kernel(const SelParams 
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) c += __popc(m[u]);
-      int incl = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      uint32_t at = 0u;
-      if (lane == 31 && incl != 0) at = atomicAdd(&s_n, static_cast<uint32_t>(incl));
-      at = __shfl_sync(0xffffffffu, at, 31) + incl - c;
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        for (uint32_t x = m[u]; x != 0u; x &= x - 1u, ++at)
-          if (at < kSelKeys) where[at] = (i0 + u * kSelThreads + tid) * 32 + __ffs(x) - 1;
     }
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0 && c != 0u) atomicAdd(&s_n, c);
     __syncthreads();
     n = s_n;
-    const bool on_chip = n <= kSelKeys;
+    sparse = n <= kSelWords / 2 && n <= 2u * nb;
+    const bool on_chip = n <= (sparse ? kSelWords / 2 : kSelWords);
+    if (sparse) {
+      for (int i0 = 0; i0 < nb; i0 += kSelThreads * U) {
+        int mine = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * kSelThreads + tid;
+          if (nb > kSelThreads * U) m[u] = i < nb ? mask[i] : 0u;   // else still at hand
+          mine += __popc(m[u]);
+        }
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += y;
+        }
+        uint32_t at = 0u;
+        if (lane == 31 && incl != 0) at = atomicAdd(&s_at, static_cast<uint32_t>(incl));
+        at = __shfl_sync(0xffffffffu, at, 31) + incl - mine;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          for (uint32_t x = m[u]; x != 0u; x &= x - 1u, ++at)
+            where[at] = (i0 + u * kSelThreads + tid) * 32 + __ffs(x) - 1;
+      }
+      __syncthreads();
+#pragma unroll 4
+      for (uint32_t i = tid; i < n; i += kSelThreads) keys[i] = order_key(score[where[i]]);
+    } else if (on_chip) {
+      walk([&](int, uint32_t x, float a) {
+        uint32_t at = 0u;
+        if (lane == 0 && x != 0u) at = atomicAdd(&s_at, static_cast<uint32_t>(__popc(x)));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(x & ((1u << lane) - 1u));
+        if ((x >> lane) & 1u) keys[at] = order_key(a);
+      });
+      __syncthreads();
+    }
     const auto each = [&](auto f) {             // f(order key)
       if (on_chip) {
         for (uint32_t i = tid; i < n; i += kSelThreads) f(keys[i]);
       } else {
-        for (int i = tid; i < nb; i += kSelThreads)
-          for (uint32_t x = mask[i]; x != 0u; x &= x - 1u) f(order_key(score[i * 32 + __ffs(x) - 1]));
+        walk([&](int, uint32_t x, float a) { if ((x >> lane) & 1u) f(order_key(a)); });
       }
     };
-    if (on_chip) {
-#pragma unroll 4
-      for (uint32_t i = tid; i < n; i += kSelThreads) keys[i] = order_key(score[where[i]]);
-    }
-    uint32_t mx = 0u;                           // a thread reads the keys it stored
+    uint32_t mx = 0u;
     each([&](uint32_t k) { mx = max(mx, k); });
     mx = cta_max(mx, &s_max);
     // (-0 and +0 compare equal in the scan: the bound's key is the lower one)
@@ -422,16 +453,14 @@ __global__ void __launch_bounds__(kSelThreads) q4_select_kernel(const SelParams 
   if (p.keep == 0) return;
   if (p.N < L) {
     const uint32_t k_tau = order_key(tau == 0.f ? -0.f : tau);
-    if (n <= kSelKeys) {
+    if (sparse) {
       for (uint32_t i = tid; i < n; i += kSelThreads)
         if (keys[i] < k_tau) atomicAnd(&mask[where[i] / 32], ~(1u << (where[i] % 32)));
     } else {
-      for (int i = tid; i < nb; i += kSelThreads) {
-        uint32_t kept = 0u;
-        for (uint32_t x = mask[i]; x != 0u; x &= x - 1u)
-          if (order_key(score[i * 32 + __ffs(x) - 1]) >= k_tau) kept |= x & (0u - x);
-        mask[i] = kept;
-      }
+      walk([&](int i, uint32_t x, float a) {
+        const uint32_t kept = __ballot_sync(0xffffffffu, (x >> lane) & 1u && order_key(a) >= k_tau);
+        if (lane == 0) mask[i] = kept;
+      });
     }
   }
   if (p.sel_mask == nullptr) return;
@@ -484,7 +513,7 @@ cudaError_t launch_q4_bound(const Q4Params &p, int32_t N, float *bound, cudaStre
 cudaError_t launch_q4_select(const Q4Params &p, int32_t N, const float *bound, float *tau, bool keep,
                              uint8_t *sel_mask, cudaStream_t st) {
   static std::atomic<bool> attr_set[kMaxDevices];
-  constexpr int kSmem = 2 * kSelKeys * 4;
+  constexpr int kSmem = kSelWords * 4;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
