@@ -91,7 +91,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 // d (+)= a [16 x 16] * b [16 x 8], fp16 operands, fp32 sums
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -190,41 +190,50 @@ struct Stage {
   __device__ __forceinline__ uint32_t refill_parity() const { return st >= 2 ? phase : phase ^ 1u; }
 };
 
-// Raw scores (fp16 operands' units) of 16 query rows against eight keys: this
-// lane's key row starts at `codes` and `scales` in shared memory; column c of
-// the tile is the key of the lanes with lane / 4 == c.
-template <int D, int MT, bool Q2>
-__device__ __forceinline__ void score_tile(const uint8_t *codes, const uint8_t *scales, int tq,
-                                           const uint32_t (&hi)[MT][D / 16][4],
-                                           const uint32_t (&lo)[Q2 ? MT : 1][Q2 ? D / 16 : 1][4],
-                                           float (&c)[MT][4]) {
-  uint32_t w[D / 32];
-  uint32_t sb;
-  if constexpr (D == 64) {
-    const uint2 x = *reinterpret_cast<const uint2 *>(codes + tq * 8);
-    w[0] = x.x; w[1] = x.y;
-    sb = scales[tq];
-  } else {
-    const uint4 x = *reinterpret_cast<const uint4 *>(codes + tq * 16);
-    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-    sb = *reinterpret_cast<const uint16_t *>(scales + tq * 2);
+// Raw scores (fp16 operands' units) of 16 MT query rows against 8 NT keys: this
+// lane's key row of the first tile starts at `codes` and `scales` in shared
+// memory, those of the others eight rows apart; column c of a tile is the key of
+// the lanes with lane / 4 == c. The tiles' MMAs alternate: each depends on the
+// one before it in its own tile only.
+template <int D, int MT, int NT, bool Q2>
+__device__ __forceinline__ void score_tiles(const uint8_t *codes, const uint8_t *scales, int tq,
+                                            const uint32_t (&hi)[MT][D / 16][4],
+                                            const uint32_t (&lo)[Q2 ? MT : 1][Q2 ? D / 16 : 1][4],
+                                            float (&c)[NT][MT][4]) {
+  uint32_t w[NT][D / 32], sb[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    if constexpr (D == 64) {
+      const uint2 x = *reinterpret_cast<const uint2 *>(codes + t * 8 * (D / 2) + tq * 8);
+      w[t][0] = x.x; w[t][1] = x.y;
+      sb[t] = scales[t * 8 * (D / 16) + tq];
+    } else {
+      const uint4 x = *reinterpret_cast<const uint4 *>(codes + t * 8 * (D / 2) + tq * 16);
+      w[t][0] = x.x; w[t][1] = x.y; w[t][2] = x.z; w[t][3] = x.w;
+      sb[t] = *reinterpret_cast<const uint16_t *>(scales + t * 8 * (D / 16) + tq * 2);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) c[t][m][0] = c[t][m][1] = c[t][m][2] = c[t][m][3] = 0.f;
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m) c[m][0] = c[m][1] = c[m][2] = c[m][3] = 0.f;
-#pragma unroll
   for (int i = 0; i < D / 32; ++i) {
-    const uint32_t sc = scale_f16(i < 2 ? sb : sb >> 8);
-    uint32_t h[4];
-    codes_f16(w[i], h);
+    uint32_t h[NT][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = mul_f16x2(h[e], sc);
+    for (int t = 0; t < NT; ++t) {
+      const uint32_t sc = scale_f16(i < 2 ? sb[t] : sb[t] >> 8);
+      codes_f16(w[t][i], h[t]);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int e = 0; e < 4; ++e) h[t][e] = mul_f16x2(h[t][e], sc);
+    }
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        mma(c[m], hi[m][2 * i + t], h[2 * t], h[2 * t + 1]);
-        if constexpr (Q2) mma(c[m], lo[m][2 * i + t], h[2 * t], h[2 * t + 1]);
-      }
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int q = 0; q < (Q2 ? 2 : 1); ++q)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            mma(c[t][m], q == 0 ? hi[m][2 * i + k] : lo[Q2 ? m : 0][Q2 ? 2 * i + k : 0], h[t][2 * k], h[t][2 * k + 1]);
   }
 }
 

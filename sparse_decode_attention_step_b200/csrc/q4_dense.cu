@@ -215,16 +215,16 @@ q4_dense_kernel(const Q4Params p) {
 
         // ---- scores of the warp's keys: x[tile][key tile][2 keys of this lane] -------
         float x[NRT][NT][2];
+        {
+          float d[NT][MT][4];
+          q4::score_tiles<D, MT, NT, Q2>(kc + key * (D / 2), ks + key * (D / 16), tq, qh, ql, d);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float d[MT][4];
-          q4::score_tile<D, MT, Q2>(kc + (8 * nt + key) * (D / 2), ks + (8 * nt + key) * (D / 16), tq,
-                                    qh, ql, d);
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int r = 0; r < NRT; ++r) {
-            x[r][nt][0] = d[r / 2][r % 2 * 2];
-            x[r][nt][1] = d[r / 2][r % 2 * 2 + 1];
-          }
+            for (int r = 0; r < NRT; ++r) {
+              x[r][nt][0] = d[nt][r / 2][r % 2 * 2];
+              x[r][nt][1] = d[nt][r / 2][r % 2 * 2 + 1];
+            }
         }
         if (left < C::kKeys) {                 // columns 2 tq, 2 tq + 1 are keys tq, tq + 4
 #pragma unroll
@@ -309,19 +309,25 @@ q4_dense_kernel(const Q4Params p) {
                 q4::value_pair(wa, wb, vs[r0 * (D / 16)], vs[r1 * (D / 16)], pr, a[j]);
               }
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int r = 0; r < NRT; ++r) {
+              if (MODE != kRowsL16 && r != vw) continue;
+              float t[4][4];
 #pragma unroll
-              for (int r = 0; r < NRT; ++r) {
-                if (MODE != kRowsL16 && r != vw) continue;
-                float t[4] = {0.f, 0.f, 0.f, 0.f};
+              for (int n = 0; n < 4; ++n) t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.f;
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                  q4::mma(t, a[j][n], ph[r][j][0], ph[r][j][1]);
-                  if constexpr (MODE != kRowsS) q4::mma(t, a[j][n], pl[r][j][0], pl[r][j][1]);
+              for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) q4::mma(t[n], a[j][n], ph[r][j][0], ph[r][j][1]);
+                if constexpr (MODE != kRowsS) {
+#pragma unroll
+                  for (int n = 0; n < 4; ++n) q4::mma(t[n], a[j][n], pl[r][j][0], pl[r][j][1]);
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[r][4 * u + n][e] += t[e];
               }
+#pragma unroll
+              for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[r][4 * u + n][e] += t[n][e];
+            }
           }
         }
       }

@@ -127,13 +127,17 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) q4_gather_kernel(co
         for (int pr = 0; pr < 2; ++pr)
           q4::value_pair(r.code[j][2 * pr][u], r.code[j][2 * pr + 1][u], r.scale[j][2 * pr], r.scale[j][2 * pr + 1],
                          pr, a[j]);
+      float t[4][4];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int n = 0; n < 4; ++n) q4::mma(t[n], a[j][n], pb[j][0], pb[j][1]);
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        float t[4] = {0.f, 0.f, 0.f, 0.f};
-        q4::mma(t, a[0][n], pb[0][0], pb[0][1]);
-        q4::mma(t, a[1][n], pb[1][0], pb[1][1]);
-        acc[4 * u + n][0] += t[0] + t[1];        // lanes with tq == 0 hold columns 0 and 1
-        acc[4 * u + n][1] += t[2] + t[3];
+        acc[4 * u + n][0] += t[n][0] + t[n][1];  // lanes with tq == 0 hold columns 0 and 1
+        acc[4 * u + n][1] += t[n][2] + t[n][3];
       }
     }
   };

@@ -137,13 +137,12 @@ __global__ void __launch_bounds__(kThreads, kQ4ScanCtasPerSm) q4_scan_kernel(con
       if (rest > 0) {
         const uint8_t *codes = ring + at.st * C::kStage + (warp * 32 + g) * (D / 2);
         const uint8_t *scales = ring + at.st * C::kStage + C::kCodes + (warp * 32 + g) * (D / 16);
+        float d[4][1][4];
+        q4::score_tiles<D, 1, 4, Q2>(codes, scales, tq, qh, ql, d);
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) {
-          float d[1][4];
-          q4::score_tile<D, 1, Q2>(codes + 8 * nt * (D / 2), scales + 8 * nt * (D / 16), tq, qh, ql, d);
+        for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[nt][e] = d[0][e];
-        }
+          for (int e = 0; e < 4; ++e) x[nt][e] = d[nt][0][e];
       }
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(&bars.empty[at.st]);
