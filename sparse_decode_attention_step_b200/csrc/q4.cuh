@@ -337,7 +337,7 @@ struct Piece {
 
 template <int CH>
 __device__ __forceinline__ Piece next_piece(const Q4Params &p, Seq &s, int64_t &x, int64_t end) {
-  while (x >= s.start + static_cast<int64_t>(s.nb) * p.h_k) {       // sequences without a chunk fall out
+  while (x >= s.start + static_cast<int64_t>(s.nb) * p.h_k && s.b + 1 < p.B) {   // sequences without a chunk fall out
     s.start += static_cast<int64_t>(s.nb) * p.h_k;
     s.L = length(p, ++s.b, false);
     s.nb = chunks_of<CH>(s.L);

@@ -216,7 +216,8 @@ template <typename F>
 __device__ __forceinline__ uint32_t nth_largest(uint32_t lo, uint32_t hi, uint32_t N, Nth &sh, F each) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) { sh.bin = 0u; sh.rem = N; }
-  for (;;) {
+  if (hi < lo) return lo;        // fewer keys than N: scores of NaN, which nothing orders
+  for (;;) {                     // every turn leaves hi - lo < 2^shift, ten bits less
     const int shift = hi - lo < kBins ? 0 : 32 - __clz(hi - lo) - 10;
 #pragma unroll
     for (int e = 0; e < kBinsPer; ++e) sh.hist[tid + e * kSelThreads] = 0u;

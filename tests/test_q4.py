@@ -403,6 +403,75 @@ def test_step_long_rows():
     check_step(P, P.out, cnt, mask, tau, rows=[0, 5, 15])
 
 
+@pytest.mark.parametrize("N", [1, 40, 700])
+def test_nan_and_infinite_queries_stay_in_their_rows(N):
+    """A query row of NaN or infinities leaves its own outputs undefined, ends like
+    any other, and changes no other row."""
+    P = Problem(2, 16, 2, 4, 64, saga.SAGA_F32, 1300, [1300, 900], 19)
+    tau = torch.zeros(2, 16, device="cuda")
+    cnt = torch.zeros(2, 16, dtype=torch.int32, device="cuda")
+
+    def run():
+        saga.q4_refresh_threshold(P.shp, P.cache, P.q, P.l, N, tau, P.ws, out=P.out, sel_count=cnt)
+        a = (tau.clone(), P.out.clone(), cnt.clone())
+        saga.q4_decode_step(P.shp, P.cache, P.q, P.l, tau, P.out, P.ws, sel_count=cnt)
+        b = (P.out.clone(), cnt.clone())
+        saga.q4_dense_decode(P.shp, P.cache, P.q, P.l, P.out, P.ws)
+        return a + b + (P.out.clone(),)
+    clean = run()
+    P.q[0, 1, 3] = float("nan")
+    P.q[0, 9, :] = float("nan")
+    P.q[1, 2, 5] = float("inf")
+    P.q[1, 14, :] = float("-inf")
+    got = run()
+    assert saga.read_device_error(P.ws) == 0
+    ok = torch.ones(2, 16, dtype=torch.bool)
+    for b, j in ((0, 1), (0, 9), (1, 2), (1, 14)):
+        ok[b, j] = False
+    for x, y in zip(got, clean):
+        assert torch.equal(x.cpu()[ok], y.cpu()[ok])
+
+
+@pytest.mark.parametrize("N", [1, 9000, 19999])
+def test_refresh_of_rows_of_one_score(N):
+    """Every score tied: each list holds the whole row, which is too long for the chip."""
+    P = Problem(2, 8, 1, 2, 64, saga.SAGA_BF16, 20000, [20000, 12000], 23)
+    for t in (P.cache.k_codes, P.cache.k_scales):
+        t.copy_(t[:, :, :1].expand_as(t).clone())
+    P.K[:] = P.K[:, :, :1]
+    tau = torch.zeros(2, 8, device="cuda")
+    cnt = torch.zeros(2, 8, dtype=torch.int32, device="cuda")
+    saga.q4_refresh_threshold(P.shp, P.cache, P.q, P.l, N, tau, P.ws, out=P.out, sel_count=cnt)
+    for b in range(2):
+        assert cnt[b].tolist() == [int(P.lens[b])] * 8
+        for j in range(8):
+            if N >= P.lens[b]:
+                assert tau[b, j] == -np.inf
+            else:
+                assert abs(float(tau[b, j]) - P.scores(b, j)[0]) <= P.delta(b, j)
+    P.check_all(P.out)
+
+
+@pytest.mark.parametrize("N", [3000, 9000, 15000])
+def test_refresh_with_a_large_share_kept(N):
+    """Lists that do not fit the chip, dense and sparse, against the sorted score rows."""
+    P = Problem(2, 8, 1, 2, 64, saga.SAGA_BF16, 60000, [60000, 16001], 29)
+    tau = torch.zeros(2, 8, device="cuda")
+    rows = torch.zeros(2, 8, 60000, device="cuda")
+    cnt = torch.zeros(2, 8, dtype=torch.int32, device="cuda")
+    mask = torch.full((2, 8, 60000), 2, dtype=torch.uint8, device="cuda")
+    saga.q4_refresh_threshold(P.shp, P.cache, P.q, P.l, N, tau, P.ws, out=P.out, sel_count=cnt, sel_mask=mask,
+                              scores=rows)
+    for b in range(2):
+        L = int(P.lens[b])
+        s = rows[b, :, :L].sort(-1, descending=True).values
+        assert torch.equal(tau[b], s[:, N - 1])
+        assert torch.equal(mask[b, :, :L], (rows[b, :, :L] >= tau[b, :, None]).to(torch.uint8))
+        assert torch.all(mask[b, :, L:] == 2)
+        assert torch.equal(cnt[b], (rows[b, :, :L] >= tau[b, :, None]).sum(-1, dtype=torch.int32))
+    check_step(P, P.out, cnt, mask, tau, rows=[0, 7])
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
