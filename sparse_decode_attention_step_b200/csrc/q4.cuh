@@ -185,9 +185,10 @@ struct Stage {
   __device__ __forceinline__ void advance() {
     if (++st == ST) { st = 0; phase ^= 1u; }
   }
-  // the stage two before this one, and the parity of its last use's end
-  __device__ __forceinline__ int refill() const { return st >= 2 ? st - 2 : st + ST - 2; }
-  __device__ __forceinline__ uint32_t refill_parity() const { return st >= 2 ? phase : phase ^ 1u; }
+  // the stage to refill, and the parity of its last use's end
+  static constexpr int kBack = ST >= 3 ? 2 : 1;
+  __device__ __forceinline__ int refill() const { return st >= kBack ? st - kBack : st + ST - kBack; }
+  __device__ __forceinline__ uint32_t refill_parity() const { return st >= kBack ? phase : phase ^ 1u; }
 };
 
 // Raw scores (fp16 operands' units) of 16 MT query rows against 8 NT keys: this
@@ -359,11 +360,11 @@ __device__ __forceinline__ Piece next_piece(const Q4Params &p, Seq &s, int64_t &
 // one more before each, by a lane of warp i % kWarps, so that no warp is slower
 // than the others (a warp of its own for the copies would cost every thread an
 // eighth of its registers). A stage is refilled when the chunk two before the
-// current one has been read by all warps.
+// current one has been read by all warps (with two stages, the chunk before it).
 template <int CH, int ST>
 struct Ring {
-  static constexpr int kAhead = ST - 2;
-  static_assert(ST >= 3, "a stage to fill, a stage to read and one between");
+  static constexpr int kAhead = ST >= 3 ? ST - 2 : 1;
+  static_assert(ST >= 2, "a stage to fill and a stage to read");
   uint64_t full[ST], empty[ST];
   int abort;
 

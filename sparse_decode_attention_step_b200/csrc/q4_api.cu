@@ -63,7 +63,7 @@ Q4Plan q4_plan(const saga_shape &s) {
   p.SB = static_cast<int>(ceil_div(p.nblk, p.blk_per_split));
   p.dense = 0;
   if (dense_supports(s.h_q, s.h_k, s.h_v))
-    p.dense = ctas_for(s, q4_dense_chunk(s.d, s.h_q, s.h_k, s.h_v), q4_dense_ctas_per_sm(s.d, s.h_q, s.h_k, s.h_v));
+    p.dense = ctas_for(s, q4_dense_chunk(s.d, s.h_q, s.h_k, s.h_v), kQ4DenseCtasPerSm);
   const size_t rec = static_cast<size_t>(s.d + kRecPad) * sizeof(float);
   const size_t rows = items, lists = rows * p.nblk;
   // a dense CTA leaves a record for each query head of a row it shares: at most

@@ -6,7 +6,7 @@
 // share leaves a record per CTA for the combine kernel below. Chunks of positions
 // (codes and scales of the key head and its VPG value heads, each a contiguous
 // range) come through a ring of shared-memory stages with untiled bulk copies
-// (see Ring). Eight warps each own 32 (or 16) positions of a chunk (and, with four
+// (see Ring). Eight warps each own a run of a chunk's positions (and, with four
 // value heads, two of them) and keep their own running softmax,
 // so they meet only at the ring and at the end of a row. A warp works in
 // registers throughout:
@@ -63,21 +63,25 @@ struct QD {
   static constexpr int NRT = MODE == kRowsL16 ? 2 : VPW;        // 8-row score tiles per warp
   static constexpr int MT = (NRT + 1) / 2;                      // 16-row MMA tiles
   static constexpr int NM = D / 16;                             // 16-dim MMA tiles of the output
-  static constexpr int kKeys = D == 128 && NRT == 1 ? 16 : 32;  // positions per warp and chunk (16: room for the ring)
+  // Positions per warp and chunk. One CTA per SM, whose eight warps have up to 255
+  // registers each, is as fast as two with half of that or as 12 and 16 warps, and
+  // long runs of positions spread a chunk's fixed work (waits, the running maximum,
+  // addresses: a hundred instructions): 8 x 128K positions of 8 + 8 heads of 64 took
+  // 161 us with 32 at a time, 147 with 48 and 142 with 128. As many as leave two or
+  // three stages of the ring room and the accumulators their registers.
+  static constexpr int kKeys = D == 64 ? (VPG == 1 ? 128 : 80) : (VPG == 1 ? 64 : VPG == 2 ? 32 : 48);
   static constexpr int NT = kKeys / 8, NJ = kKeys / 16;         // key tiles, 16-key steps
   static constexpr int KC = SL * kKeys;
   static constexpr int kCodes = KC * D / 2, kScales = KC * D / 16;
   static constexpr int kStage = (kCodes + kScales) * (1 + VPG);
-  // two CTAs per SM where the registers allow (the accumulators of a warp are
-  // 16 per score tile at d = 64, 32 at d = 128)
-  static constexpr int kCtas = NRT * NM <= 8 ? 2 : 1;
   static constexpr int kState = NRT * (NM * 4 + 2);             // a warp's registers to merge
-  static constexpr int kMerge = kWarps / 2 * kState * 32 * 4;
-  static constexpr int kBudget = (kCtas == 2 ? 108 * 1024 : 216 * 1024) - kMerge;
-  static constexpr int kStages = kBudget / kStage < 8 ? kBudget / kStage : 8;
+  static constexpr int kSlot = NG * kState * 32 * 4;            // a slab's states
+  static constexpr int kSpace = 230400;                         // shared memory of a CTA, less its barriers
+  static constexpr int kStages = (kSpace - kSlot) / kStage < 8 ? (kSpace - kSlot) / kStage : 8;
   static constexpr int kRing = kStages * kStage;
-  static constexpr int kSmem = kRing + kMerge;
-  static_assert(kStages >= 3, "a ring");
+  static constexpr int kSlots = (kSpace - kRing) / kSlot < SL / 2 ? (kSpace - kRing) / kSlot : SL / 2;
+  static constexpr int kSmem = kRing + kSlots * kSlot;
+  static_assert(kStages >= 2 && kSlots >= 1, "a ring and a slab's states");
 };
 
 // Merge a second running softmax state (m2, l2, and acc2 by f(register)) into
@@ -99,7 +103,7 @@ __device__ __forceinline__ void merge_state(float &m, float &l, float (&acc)[NM]
 }
 
 template <int D, int VPW, int MODE, int NG, typename T>
-__global__ void __launch_bounds__(kThreads, QD<D, VPW, MODE, NG>::kCtas)
+__global__ void __launch_bounds__(kThreads, 1)
 q4_dense_kernel(const Q4Params p) {
   using C = QD<D, VPW, MODE, NG>;
   constexpr bool Q2 = sizeof(T) == 4;
@@ -117,6 +121,9 @@ q4_dense_kernel(const Q4Params p) {
 
   const int cta = blockIdx.x;
   const q4::Work work = q4::work_of<KC>(p, lane, cta == 0 && warp == 0);
+  for (int b = cta; b < p.B; b += gridDim.x)         // an empty sequence: zero rows
+    if (q4::length(p, b, false) == 0)
+      for (int i = tid; i < p.h_q * D; i += kThreads) p.out[static_cast<int64_t>(b) * p.h_q * D + i] = 0.f;
   if (cta >= work.n) return;
   int64_t x0 = work.begin(cta);
   const int64_t x1 = work.begin(cta + 1);
@@ -343,26 +350,31 @@ q4_dense_kernel(const Q4Params p) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
     }
 #pragma unroll
-    for (int h = C::SL / 2; h > 0; h /= 2) {
-      sm100::named_bar(1, kWarps * 32);              // the last reads of `merge` are done
-      if (slab >= h && slab < 2 * h) {
-        float *o = merge + ((slab - h) * NG + vg) * (C::kState * 32) + lane;
+    for (int n = C::SL; n > 1; n = (n + 1) / 2) {    // n slabs left: the upper half joins the lower
+      const int h = (n + 1) / 2;
 #pragma unroll
-        for (int r = 0; r < NRT; ++r) {
+      for (int s0 = h; s0 < n; s0 += C::kSlots) {    // as many at a time as there is room for
+        sm100::named_bar(1, kWarps * 32);            // the last reads of `merge` are done
+        if (slab >= s0 && slab < n && slab < s0 + C::kSlots) {
+          float *o = merge + ((slab - s0) * NG + vg) * (C::kState * 32) + lane;
 #pragma unroll
-          for (int e = 0; e < NM * 4; ++e) o[(r * (NM * 4 + 2) + e) * 32] = acc[r][e / 4][e % 4];
-          o[(r * (NM * 4 + 2) + NM * 4) * 32] = m[r];
-          o[(r * (NM * 4 + 2) + NM * 4 + 1) * 32] = l[r];
+          for (int r = 0; r < NRT; ++r) {
+#pragma unroll
+            for (int e = 0; e < NM * 4; ++e) o[(r * (NM * 4 + 2) + e) * 32] = acc[r][e / 4][e % 4];
+            o[(r * (NM * 4 + 2) + NM * 4) * 32] = m[r];
+            o[(r * (NM * 4 + 2) + NM * 4 + 1) * 32] = l[r];
+          }
         }
-      }
-      sm100::named_bar(1, kWarps * 32);
-      if (slab < h) {
-        const float *o = merge + (slab * NG + vg) * (C::kState * 32) + lane;
+        sm100::named_bar(1, kWarps * 32);
+        const int from = slab + h;                   // the slab that joins this one
+        if (from >= s0 && from < n && from < s0 + C::kSlots) {
+          const float *o = merge + ((from - s0) * NG + vg) * (C::kState * 32) + lane;
 #pragma unroll
-        for (int r = 0; r < NRT; ++r) {
-          const float *q = o + r * (NM * 4 + 2) * 32;
-          merge_state<NM>(m[r], l[r], acc[r], q[NM * 4 * 32], q[(NM * 4 + 1) * 32], tq,
-                          [&](int e) { return q[e * 32]; });
+          for (int r = 0; r < NRT; ++r) {
+            const float *q = o + r * (NM * 4 + 2) * 32;
+            merge_state<NM>(m[r], l[r], acc[r], q[NM * 4 * 32], q[(NM * 4 + 1) * 32], tq,
+                            [&](int e) { return q[e * 32]; });
+          }
         }
       }
     }
@@ -409,8 +421,7 @@ q4_dense_kernel(const Q4Params p) {
 }
 
 // Rows that several CTAs share: their records {m, l, gave up, -, acc} (m in log2
-// units) merged in CTA order; a row that no CTA had (an empty sequence) becomes
-// zero. One CTA of four warps per (b, query head).
+// units) merged in CTA order. One CTA of four warps per (b, query head).
 constexpr int kCombThreads = 128;
 constexpr int kCombWarps = kCombThreads / 32;
 
@@ -430,10 +441,7 @@ __global__ void __launch_bounds__(kCombThreads) q4_combine_kernel(const Q4Params
   for (int o = 16; o > 0; o >>= 1) start += __shfl_xor_sync(0xffffffffu, start, o);
   const int nb = q4::chunks_of<CH>(q4::length(p, b, false));
   float *out = p.out + static_cast<int64_t>(blockIdx.x) * D;
-  if (nb == 0) {
-    if (tid < D) out[tid] = 0.f;
-    return;
-  }
+  if (nb == 0) return;
   const int64_t x = start + static_cast<int64_t>(kh) * nb;
   const int i0 = work.cta_of(x), i1 = work.cta_of(x + nb - 1);
   if (i0 == i1) return;                              // written by that CTA
@@ -489,7 +497,7 @@ cudaError_t launch_cfg(const Q4Params &p, cudaStream_t st) {
     attr_set[dev].store(true, std::memory_order_release);
   }
   e = launch_pdl(q4_dense_kernel<D, VPW, MODE, NG, T>, dim3(p.S), dim3(kThreads), C::kSmem, st, p);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.max_l_kv <= C::KC) return e;   // rows of one chunk are never shared
   return launch_pdl(q4_combine_kernel<D, C::KC>, dim3(p.B * p.h_q), dim3(kCombThreads), 0, st, p);
 }
 
@@ -519,11 +527,6 @@ struct LaunchQ4 {
 int q4_dense_chunk(int d, int h_q, int h_k, int h_v) {
   auto chunk = [](auto c) { return decltype(c)::KC; };
   return d == 64 ? with_cfg<64>(h_q, h_k, h_v, chunk) : with_cfg<128>(h_q, h_k, h_v, chunk);
-}
-
-int q4_dense_ctas_per_sm(int d, int h_q, int h_k, int h_v) {
-  auto ctas = [](auto c) { return decltype(c)::kCtas; };
-  return d == 64 ? with_cfg<64>(h_q, h_k, h_v, ctas) : with_cfg<128>(h_q, h_k, h_v, ctas);
 }
 
 cudaError_t launch_q4_dense(const Q4Params &p, int dtype, int d, cudaStream_t st) {

@@ -36,9 +36,9 @@ cudaError_t launch_q4_read(const Q4Read &p, int dtype, cudaStream_t st);
 
 // Full attention by p.S CTAs, then the combine. Head layouts as dense_supports.
 cudaError_t launch_q4_dense(const Q4Params &p, int dtype, int d, cudaStream_t st);
-// The dense kernel's chunk of positions and CTAs per SM.
+// The dense kernel's chunk of positions.
 int q4_dense_chunk(int d, int h_q, int h_k, int h_v);
-int q4_dense_ctas_per_sm(int d, int h_q, int h_k, int h_v);
+constexpr int kQ4DenseCtasPerSm = 1;
 
 // Score pass by p.S CTAs: the kept lists of p.tau (step), the group maxima
 // (max), or the score rows (dump).
