@@ -260,11 +260,15 @@ saga_status saga_q4_refresh_threshold(const saga_shape *shape, const saga_q4_cac
       return cuda_fail(e, "score dump kernel (4-bit)");
   }
   // 1. the largest score of every eight positions, and the N-th largest of those:
-  // a lower bound of the threshold (-inf with N groups or fewer)
-  if ((e = launch_q4_scan(p, kQ4Max, s.dtype, s.d, st)) != cudaSuccess)
-    return cuda_fail(e, "group maximum kernel (4-bit)");
-  float *bound = reinterpret_cast<float *>(static_cast<char *>(ws) + pl.off_bound);
-  if ((e = launch_q4_bound(p, N, bound, st)) != cudaSuccess) return cuda_fail(e, "bound kernel (4-bit)");
+  // a lower bound of the threshold (-inf with N groups or fewer; for rows that the
+  // select holds on chip whole, two launches fewer without it)
+  float *bound = nullptr;
+  if (s.max_l_kv > kQ4SelectKeys) {
+    bound = reinterpret_cast<float *>(static_cast<char *>(ws) + pl.off_bound);
+    if ((e = launch_q4_scan(p, kQ4Max, s.dtype, s.d, st)) != cudaSuccess)
+      return cuda_fail(e, "group maximum kernel (4-bit)");
+    if ((e = launch_q4_bound(p, N, bound, st)) != cudaSuccess) return cuda_fail(e, "bound kernel (4-bit)");
+  }
   // 2. the scores that reach it
   p.tau = bound;
   if ((e = launch_q4_scan(p, kQ4Step, s.dtype, s.d, st)) != cudaSuccess)

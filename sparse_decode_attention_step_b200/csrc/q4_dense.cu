@@ -421,14 +421,18 @@ q4_dense_kernel(const Q4Params p) {
 }
 
 // Rows that several CTAs share: their records {m, l, gave up, -, acc} (m in log2
-// units) merged in CTA order. One CTA of four warps per (b, query head).
-constexpr int kCombThreads = 128;
+// units) merged in CTA order. One CTA per (b, query head): the largest maximum,
+// then kCombAt records' weights at a time and their sums, each thread one dim of
+// every kPar-th record with several loads under way (a row of batch 1 has a
+// record of every CTA).
+constexpr int kCombThreads = 256;
 constexpr int kCombWarps = kCombThreads / 32;
+constexpr int kCombAt = 128;
 
 template <int D, int CH>
 __global__ void __launch_bounds__(kCombThreads) q4_combine_kernel(const Q4Params p) {
-  constexpr int E = D / 32;
-  __shared__ float s_acc[kCombWarps][D], s_m[kCombWarps], s_l[kCombWarps];
+  constexpr int kPar = kCombThreads / D;
+  __shared__ float s_acc[kCombThreads], s_w[kCombAt], s_m[kCombWarps], s_l[kCombWarps];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -440,46 +444,50 @@ __global__ void __launch_bounds__(kCombThreads) q4_combine_kernel(const Q4Params
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) start += __shfl_xor_sync(0xffffffffu, start, o);
   const int nb = q4::chunks_of<CH>(q4::length(p, b, false));
-  float *out = p.out + static_cast<int64_t>(blockIdx.x) * D;
   if (nb == 0) return;
   const int64_t x = start + static_cast<int64_t>(kh) * nb;
-  const int i0 = work.cta_of(x), i1 = work.cta_of(x + nb - 1);
-  if (i0 == i1) return;                              // written by that CTA
+  const int i0 = work.cta_of(x), n = work.cta_of(x + nb - 1) - i0 + 1;
+  if (n == 1) return;                                // written by its one CTA
 
-  float m = -INFINITY, l = 0.f, a[E];
-  bool gave_up = false;
-#pragma unroll
-  for (int e = 0; e < E; ++e) a[e] = 0.f;
-  for (int i = i0 + warp; i <= i1; i += kCombWarps) {
-    const float *r = p.partials + (static_cast<int64_t>(i + b * p.h_k + kh) * G + j % G) * (D + kRecPad);
-    const float4 h = *reinterpret_cast<const float4 *>(r);
-    float v[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = r[kRecPad + e * 32 + lane];
-    gave_up |= h.z != 0.f;
-    const float mn = fmaxf(m, h.x);
-    const float ca = m == -INFINITY ? 0.f : q4::ex2(m - mn), cb = h.x == -INFINITY ? 0.f : q4::ex2(h.x - mn);
-    m = mn;
-    l = l * ca + h.y * cb;
-#pragma unroll
-    for (int e = 0; e < E; ++e) a[e] = a[e] * ca + v[e] * cb;
+  // a CTA's record of the next row follows G (D + kRecPad) floats on, and so does
+  // the next CTA's of this row
+  const int64_t step = static_cast<int64_t>(G) * (D + kRecPad);
+  const float *rec = p.partials + (i0 + b * p.h_k + kh) * step + (j % G) * (D + kRecPad);
+  float m = -INFINITY;
+  for (int i = tid; i < n; i += kCombThreads) {
+    const float4 h = *reinterpret_cast<const float4 *>(rec + i * step);
+    m = fmaxf(m, h.z != 0.f ? INFINITY : h.x);       // a CTA that gave up: NaN below
   }
+  m = warp_max(m);
+  if (lane == 0) s_m[warp] = m;
+  __syncthreads();
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_acc[warp][e * 32 + lane] = a[e];
-  if (lane == 0) { s_m[warp] = m; s_l[warp] = gave_up ? __int_as_float(0x7fc00000) : l; }
+  for (int w = 0; w < kCombWarps; ++w) m = fmaxf(m, s_m[w]);
+  float a = 0.f, l = 0.f;
+  for (int r0 = 0; r0 < n; r0 += kCombAt) {
+    const int k = min(kCombAt, n - r0);
+    __syncthreads();
+    if (tid < k) {
+      const float2 h = *reinterpret_cast<const float2 *>(rec + (r0 + tid) * step);
+      const float c = h.x == -INFINITY ? 0.f : q4::ex2(h.x - m);
+      s_w[tid] = c;
+      l = fmaf(c, h.y, l);
+    }
+    __syncthreads();
+#pragma unroll 8
+    for (int i = tid / D; i < k; i += kPar) a = fmaf(s_w[i], rec[(r0 + i) * step + kRecPad + tid % D], a);
+  }
+  l = warp_sum(l);
+  if (lane == 0) s_l[warp] = l;
+  s_acc[tid] = a;
   __syncthreads();
   if (tid >= D) return;
-  float M = s_m[0];
+  l = s_l[0];
 #pragma unroll
-  for (int w = 1; w < kCombWarps; ++w) M = fmaxf(M, s_m[w]);
-  float o = 0.f, lt = 0.f;
+  for (int w = 1; w < kCombWarps; ++w) l += s_l[w];
 #pragma unroll
-  for (int w = 0; w < kCombWarps; ++w) {
-    const float c = s_m[w] == -INFINITY ? 0.f : q4::ex2(s_m[w] - M);
-    o = fmaf(c, s_acc[w][tid], o);
-    lt = fmaf(c, s_l[w], lt);
-  }
-  out[tid] = o / lt;
+  for (int i = 1; i < kPar; ++i) a += s_acc[tid + i * D];
+  p.out[static_cast<int64_t>(blockIdx.x) * D + tid] = m == INFINITY ? __int_as_float(0x7fc00000) : a / l;
 }
 
 template <int D, int VPW, int MODE, int NG, typename T>

@@ -40,7 +40,7 @@ cudaError_t launch_q4_dense(const Q4Params &p, int dtype, int d, cudaStream_t st
 int q4_dense_chunk(int d, int h_q, int h_k, int h_v);
 constexpr int kQ4DenseCtasPerSm = 1;
 
-// Score pass by p.S CTAs: the kept lists of p.tau (step), the group maxima
+// Score pass by p.S CTAs: the kept lists of p.tau (step; -inf where it is null), the group maxima
 // (max), or the score rows (dump).
 enum { kQ4Step = 0, kQ4Max = 1, kQ4Dump = 2 };
 cudaError_t launch_q4_scan(const Q4Params &p, int mode, int dtype, int d, cudaStream_t st);
@@ -52,8 +52,9 @@ constexpr int kQ4ScanCtasPerSm = 2;
 cudaError_t launch_q4_bound(const Q4Params &p, int32_t N, float *bound, cudaStream_t st);
 
 // tau[b][j] = the N-th largest of row (b, j)'s listed scores, all of them at
-// least bound[b][j], or -inf when N >= l_kv[b]; with `keep`, the lists (and a
+// least bound[b][j] (-inf where bound is null), or -inf when N >= l_kv[b]; with `keep`, the lists (and a
 // given sel_mask) are cut down to it.
+constexpr int kQ4SelectKeys = 10240;   // scores of a row that it holds on chip
 cudaError_t launch_q4_select(const Q4Params &p, int32_t N, const float *bound, float *tau, bool keep,
                              uint8_t *sel_mask, cudaStream_t st);
 

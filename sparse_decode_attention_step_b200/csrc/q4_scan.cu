@@ -108,7 +108,8 @@ __global__ void __launch_bounds__(kThreads, kQ4ScanCtasPerSm) q4_scan_kernel(con
     fac[1] = unit * q4::q_frag<D, T, Q2, 1>(qb + 8 * p.q_sh, live[1], tq, qh[0], ql[0]);
     if (MODE == kQ4Step) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) thr[r] = live[r] ? p.tau[b * p.h_q + j0 + g + 8 * r] : INFINITY;
+      for (int r = 0; r < 2; ++r)
+        thr[r] = live[r] ? (p.tau != nullptr ? p.tau[b * p.h_q + j0 + g + 8 * r] : -INFINITY) : INFINITY;
     }
     // this lane's places in the outputs of its first head, at 32-position block
     // 0; the second is eight heads on
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) q4_bound_kernel(const BoundPar
 // its scores at once; a dense one (a short row, where N groups are most of it)
 // is read a block per warp. Lists too long for the chip (ties at the bound, or a
 // large N) are read that way again for each histogram.
-constexpr int kSelWords = 10240;                // keys, or half as many keys and positions: 40 KB, four CTAs per SM
+constexpr int kSelWords = kQ4SelectKeys;        // keys, or half as many keys and positions: 40 KB, four CTAs per SM
 
 struct SelParams {
   uint32_t *lmask;
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kSelThreads, 4) q4_select_kernel(const SelPara
   bool sparse = false;
   uint32_t n = 0u;
   if (p.N < L) {
-    const float lo = p.bound[bj];
+    const float lo = p.bound != nullptr ? p.bound[bj] : -INFINITY;
     if (tid == 0) { s_n = 0u; s_at = 0u; s_max = 0u; }
     __syncthreads();
     constexpr int U = 8;                        // masks a thread loads at once
