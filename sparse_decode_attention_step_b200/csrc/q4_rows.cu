@@ -41,12 +41,11 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
   return d;
 }
 
-// x >= 0 over t, correctly rounded, by Markstein's method (IBM J. Res. Dev. 34,
-// 1990): with `inv` the rounded reciprocal, one correction makes the quotient
-// faithful and a second one from its exact residual rounds it correctly. For t
-// within 2^+-100 the residuals neither overflow nor lose bits that matter (a
-// quotient small enough for that rounds to code 0 all the same). An infinite x
-// gives NaN, which fminf turns into 6, the largest code.
+// x / t, correctly rounded, by Markstein's method (IBM J. Res. Dev. 34, 1990):
+// with `inv` the rounded reciprocal, one correction makes the quotient faithful
+// and a second one from its exact residual rounds it correctly. For t within
+// 2^+-100 and x finite the residuals neither overflow nor lose bits that matter (a
+// quotient small enough for that rounds to code 0 all the same).
 __device__ __forceinline__ float quotient(float x, float t, float inv) {
   float q = x * inv;
   q = fmaf(fmaf(-q, t, x), inv, q);
@@ -83,35 +82,63 @@ __device__ __forceinline__ void widen(const Raw16 &r, float (&x)[16]) {
   }
 }
 
+// The largest magnitude of a block; infinite or NaN when it holds such a value.
+template <typename T>
+__device__ __forceinline__ float block_max(const Raw16 &r) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t m = 0u;                     // magnitudes order like integers, NaN above infinity
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t u[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(u[e] & 0x7fff7fffu));
+    }
+    return __uint_as_float(max(m << 16, m & 0xffff0000u));
+  } else {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(__uint_as_float(u[e]))));
+    }
+    return m;
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ void quantise_block(const Raw16 &raw, float g, uint2 *codes, uint8_t *scale) {
   float x[16];
   widen<T>(raw, x);
-  float mx = 0.f;
-  uint32_t sign[2] = {0u, 0u};
+  float mx = block_max<T>(raw);
+  const bool finite = mx < INFINITY;
+  if (!finite) {                         // NaN counts as zero
+    mx = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if (x[i] != x[i]) x[i] = 0.f;                            // NaN counts as zero
-    sign[i / 8] |= (__float_as_uint(x[i]) >> 31) << (i % 8 * 4 + 3);
-    x[i] = fabsf(x[i]);
-    mx = fmaxf(mx, x[i]);
+    for (int i = 0; i < 16; ++i) {
+      if (x[i] != x[i]) x[i] = 0.f;
+      mx = fmaxf(mx, fabsf(x[i]));
+    }
   }
   const uint32_t s = e4m3(fminf(448.f, __fdiv_rn(mx, __fmul_rn(6.f, g))));
   const float t = __fmul_rn(e4m3_value(s), g);
   uint32_t w[2] = {0u, 0u};
   if (s != 0u) {
-    if (t > 0x1p-100f && t < 0x1p100f) {
+    if (finite && t > 0x1p-100f && t < 0x1p100f) {
       const float inv = __frcp_rn(t);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = fminf(quotient(x[i], t, inv), 6.f);
+      for (int i = 0; i < 16; ++i) x[i] = quotient(x[i], t, inv);
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = fminf(__fdiv_rn(x[i], t), 6.f);
+      for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], t);
     }
+    // the conversion takes the sign along and everything above 6 to 6
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) w[i / 8] |= e2m1x2(x[i], x[i + 1]) << (i % 8 * 4);
-    w[0] |= sign[0];
-    w[1] |= sign[1];
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t lo = __byte_perm(e2m1x2(x[8 * i], x[8 * i + 1]), e2m1x2(x[8 * i + 2], x[8 * i + 3]), 0x0040);
+      const uint32_t hi = __byte_perm(e2m1x2(x[8 * i + 4], x[8 * i + 5]), e2m1x2(x[8 * i + 6], x[8 * i + 7]), 0x0040);
+      w[i] = __byte_perm(lo, hi, 0x5410);
+    }
   }
   *codes = make_uint2(w[0], w[1]);
   *scale = static_cast<uint8_t>(s);
