@@ -264,7 +264,7 @@ def step_kernel_sources():
     """The sources the decode step's kernels and plan are built from."""
     here = os.path.join(ROOT, "sparse_decode_attention_step_b200", "csrc")
     return [os.path.join(here, f) for f in ("common.cuh", "sm100.cuh", "kernels.h",
-                                            "plan.h", "q4.cuh", "saga_api.cu", "saga_tc.cu", "gather.cu",
+                                            "plan.h", "saga_api.cu", "saga_tc.cu", "gather.cu",
                                             "combine.cu")]
 
 
