@@ -98,6 +98,15 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// d = a * b: the first step of a sum, without registers of zeros
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // A query row's share of this lane: dims tq * D/4 .. + D/4 - 1 as fp32.
 template <int D>
 __device__ __forceinline__ void load_q(const float *row, int tq, float (&v)[D / 4]) {
@@ -213,8 +222,6 @@ __device__ __forceinline__ void score_tiles(const uint8_t *codes, const uint8_t 
       w[t][0] = x.x; w[t][1] = x.y; w[t][2] = x.z; w[t][3] = x.w;
       sb[t] = *reinterpret_cast<const uint16_t *>(scales + t * 8 * (D / 16) + tq * 2);
     }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) c[t][m][0] = c[t][m][1] = c[t][m][2] = c[t][m][3] = 0.f;
   }
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
@@ -233,8 +240,10 @@ __device__ __forceinline__ void score_tiles(const uint8_t *codes, const uint8_t 
 #pragma unroll
         for (int q = 0; q < (Q2 ? 2 : 1); ++q)
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-            mma(c[t][m], q == 0 ? hi[m][2 * i + k] : lo[Q2 ? m : 0][Q2 ? 2 * i + k : 0], h[t][2 * k], h[t][2 * k + 1]);
+          for (int t = 0; t < NT; ++t) {
+            if (i == 0 && k == 0 && q == 0) mma_first(c[t][m], hi[m][0], h[t][0], h[t][1]);
+            else mma(c[t][m], q == 0 ? hi[m][2 * i + k] : lo[Q2 ? m : 0][Q2 ? 2 * i + k : 0], h[t][2 * k], h[t][2 * k + 1]);
+          }
   }
 }
 

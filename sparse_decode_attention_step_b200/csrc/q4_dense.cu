@@ -320,11 +320,12 @@ q4_dense_kernel(const Q4Params p) {
               if (MODE != kRowsL16 && r != vw) continue;
               float t[4][4];
 #pragma unroll
-              for (int n = 0; n < 4; ++n) t[n][0] = t[n][1] = t[n][2] = t[n][3] = 0.f;
-#pragma unroll
               for (int j = 0; j < NJ; ++j) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n) q4::mma(t[n], a[j][n], ph[r][j][0], ph[r][j][1]);
+                for (int n = 0; n < 4; ++n) {
+                  if (j == 0) q4::mma_first(t[n], a[j][n], ph[r][j][0], ph[r][j][1]);
+                  else q4::mma(t[n], a[j][n], ph[r][j][0], ph[r][j][1]);
+                }
                 if constexpr (MODE != kRowsS) {
 #pragma unroll
                   for (int n = 0; n < 4; ++n) q4::mma(t[n], a[j][n], pl[r][j][0], pl[r][j][1]);
