@@ -36,8 +36,8 @@
  *                        They must be multiples of 256.
  *   cap                  a multiple of 4.
  * saga_shape_contiguous gives such strides for every cap that is a multiple of 4.
- * A shape that is valid in saga.h but breaks the last two gets
- * SAGA_ERR_UNSUPPORTED.
+ * A shape that is valid in saga.h but breaks the last two, or has B (h_k + h_v)
+ * above 65535 or max_l_kv above 2^31 - 4097, gets SAGA_ERR_UNSUPPORTED.
  */
 #ifndef SAGA_Q4_H_
 #define SAGA_Q4_H_
@@ -81,8 +81,8 @@ size_t saga_q4_workspace_size(const saga_shape *shape);
  *   l_kv          [B] int32, read and written.
  *   ws            a workspace (only its error word is used; >= 256 bytes).
  * A sequence that is left as it is, with the error word's bit set: l_kv[b]
- * < 0 or n < 0 (SAGA_DEVERR_LKV_NEGATIVE), n > T or l_kv[b] + n > cap
- * (SAGA_DEVERR_LKV_TOO_LONG).
+ * < 0 or n < 0 (SAGA_DEVERR_LKV_NEGATIVE), n > T or l_kv[b] + n above cap or
+ * 2^31 - 1 (SAGA_DEVERR_LKV_TOO_LONG).
  */
 saga_status saga_q4_append_kv(const saga_shape *shape, const saga_q4_cache *cache,
                               const void *k_new, const void *v_new, int32_t T,

@@ -19,6 +19,8 @@ saga_status check_q4_shape(const saga_shape *shape) {
   if (s.k_stride_b % 256 != 0 || s.k_stride_h % 256 != 0 || s.v_stride_b % 256 != 0 ||
       s.v_stride_h % 256 != 0 || s.cap % 4 != 0)
     return SAGA_ERR_UNSUPPORTED;
+  // positions and the ends of the last chunk fit an int
+  if (s.max_l_kv > INT32_MAX - 4096) return SAGA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(s.B) * (s.h_k + s.h_v) > 65535) return SAGA_ERR_UNSUPPORTED;
   return SAGA_OK;
 }

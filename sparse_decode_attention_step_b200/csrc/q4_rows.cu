@@ -44,8 +44,8 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
 // x / t, correctly rounded, by Markstein's method (IBM J. Res. Dev. 34, 1990):
 // with `inv` the rounded reciprocal, one correction makes the quotient faithful
 // and a second one from its exact residual rounds it correctly. For t within
-// 2^+-100 and x finite the residuals neither overflow nor lose bits that matter (a
-// quotient small enough for that rounds to code 0 all the same).
+// 2^+-100 and |x| <= 8 t the residuals neither overflow nor lose bits that matter
+// (a quotient small enough for that rounds to code 0 all the same).
 __device__ __forceinline__ float quotient(float x, float t, float inv) {
   float q = x * inv;
   q = fmaf(fmaf(-q, t, x), inv, q);
@@ -124,7 +124,8 @@ __device__ __forceinline__ void quantise_block(const Raw16 &raw, float g, uint2 
   const float t = __fmul_rn(e4m3_value(s), g);
   uint32_t w[2] = {0u, 0u};
   if (s != 0u) {
-    if (finite && t > 0x1p-100f && t < 0x1p100f) {
+    // a block's maximum is about 6 t, and more only where its scale stopped at 448
+    if (finite && t > 0x1p-100f && t < 0x1p100f && mx <= 8.f * t) {
       const float inv = __frcp_rn(t);
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = quotient(x[i], t, inv);
@@ -151,7 +152,7 @@ __device__ __forceinline__ int64_t append_rows(const Q4Append &p, int b, int64_t
   *at = l;
   int bad = 0;
   if (l < 0 || n < 0) bad = SAGA_DEVERR_LKV_NEGATIVE;
-  else if (n > p.T || l + n > p.cap) bad = SAGA_DEVERR_LKV_TOO_LONG;
+  else if (n > p.T || l + n > p.cap || l + n > INT32_MAX) bad = SAGA_DEVERR_LKV_TOO_LONG;
   if (bad != 0 && report) atomicOr(p.err, bad);
   return bad != 0 ? 0 : n;
 }

@@ -199,6 +199,25 @@ def test_append_special_values():
             assert np.array_equal(scales.cpu().numpy()[b, :, a:a + 200], wsc[b].transpose(1, 0, 2))
 
 
+@pytest.mark.parametrize("dtype", [saga.SAGA_BF16, saga.SAGA_F32])
+@pytest.mark.parametrize("g_exp,x_exp", [(-105, 126), (-105, 0), (-120, -100), (100, 126), (120, 0), (0, -120)])
+def test_append_far_from_the_scales_range(dtype, g_exp, x_exp):
+    # quotients that overflow, scales that stop at 448 or vanish, t outside of the fast path
+    shp = saga.shape(1, 2, 1, 2, 64, dtype, 64)
+    rng = np.random.default_rng(9)
+    x = {k: stored(rng.uniform(-1, 1, (1, 50, h, 64)) * 2.0 ** x_exp, dtype) for k, h in (("k", 1), ("v", 2))}
+    g = {"k": np.full(1, 2.0 ** g_exp, np.float32), "v": np.full(2, 1.25 * 2.0 ** g_exp, np.float32)}
+    cache = saga.Q4Cache(shp, k_g=torch.from_numpy(g["k"]).cuda(), v_g=torch.from_numpy(g["v"]).cuda())
+    l = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = saga.Q4Workspace(shp)
+    saga.q4_append_kv(shp, cache, dev(x["k"], dtype), dev(x["v"], dtype), 50, l, ws)
+    assert saga.read_device_error(ws) == 0
+    for kind, codes, scales in (("k", cache.k_codes, cache.k_scales), ("v", cache.v_codes, cache.v_scales)):
+        wc, wsc = q4.quantise(x[kind].numpy(), g[kind][None, None, :, None])
+        assert np.array_equal(codes.cpu().numpy()[0, :, :50], wc[0].transpose(1, 0, 2))
+        assert np.array_equal(scales.cpu().numpy()[0, :, :50], wsc[0].transpose(1, 0, 2))
+
+
 @pytest.mark.parametrize("T", [1, 300])
 def test_append_leaves_a_sequence_without_room(T):
     # full, negative length, n > T, n < 0, and one that fits to the last row

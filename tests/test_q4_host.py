@@ -108,3 +108,12 @@ def test_dense_head_layouts(lib, hq, hk, hv, ok):
     want = saga.SAGA_ERR_WORKSPACE if ok else saga.SAGA_ERR_UNSUPPORTED
     assert calls(lib)["dense"](s, cache(), ws=None) == want
     assert calls(lib)["step"](s, cache(), ws=None) == saga.SAGA_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_longest_rows(lib, name):
+    n = 2 ** 31 - 4096
+    call = calls(lib)[name]
+    assert call(good_shape(B=1, cap=n), cache(), ws=None) == saga.SAGA_ERR_UNSUPPORTED
+    assert call(saga.shape(1, 16, 2, 4, 64, saga.SAGA_BF16, n, max_l_kv=n - 1), cache(), ws=None) == \
+        saga.SAGA_ERR_WORKSPACE
