@@ -58,7 +58,7 @@ Q4Plan q4_plan(const saga_shape &s) {
   Q4Plan p;
   const int64_t items = static_cast<int64_t>(s.B) * s.h_q;
   p.nblk = std::max<int64_t>(1, ceil_div(s.max_l_kv, 32));
-  p.scan = ctas_for(s, kQ4ScanChunk, kQ4ScanCtasPerSm);
+  p.scan = ctas_for(s, q4_scan_chunk(s.d), kQ4ScanCtasPerSm);
   const int64_t sb = std::min(std::max<int64_t>(1, p.nblk / kGatherBlocks),
                               std::max<int64_t>(1, kGatherCtasPerSm * kSms / items));
   p.blk_per_split = ceil_div(p.nblk, sb);

@@ -44,7 +44,7 @@ constexpr int kQ4DenseCtasPerSm = 1;
 // (max), or the score rows (dump).
 enum { kQ4Step = 0, kQ4Max = 1, kQ4Dump = 2 };
 cudaError_t launch_q4_scan(const Q4Params &p, int mode, int dtype, int d, cudaStream_t st);
-constexpr int kQ4ScanChunk = 256;
+constexpr int q4_scan_chunk(int d) { return d == 64 ? 512 : 256; }
 constexpr int kQ4ScanCtasPerSm = 2;
 
 // bound[b][j]: a lower bound of the N-th largest score of row (b, j), from the

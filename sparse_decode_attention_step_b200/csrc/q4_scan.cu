@@ -38,15 +38,16 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kChunk = kQ4ScanChunk;
 constexpr int kMaxDevices = 64;
-static_assert(kChunk == kWarps * 32, "a 32-position block per warp");
 
 template <int D>
 struct QS {
+  static constexpr int kBlocks = D == 64 ? 2 : 1;               // 32-position blocks per warp and chunk
+  static constexpr int kChunk = q4_scan_chunk(D);
+  static_assert(kChunk == kWarps * kBlocks * 32, "a chunk's blocks");
   static constexpr int kCodes = kChunk * D / 2, kScales = kChunk * D / 16;
   static constexpr int kStage = kCodes + kScales;               // 9 KB (d 64), 18 KB
-  static constexpr int kStages = D == 64 ? 8 : 5;
+  static constexpr int kStages = D == 64 ? 4 : 5;
   static constexpr int kRing = kStages * kStage;                // 72, 90 KB: two CTAs per SM
 };
 
@@ -54,7 +55,7 @@ template <int D, int MODE, typename T>
 __global__ void __launch_bounds__(kThreads, kQ4ScanCtasPerSm) q4_scan_kernel(const Q4Params p) {
   using C = QS<D>;
   constexpr bool Q2 = sizeof(T) == 4;
-  constexpr int ST = C::kStages;
+  constexpr int ST = C::kStages, kChunk = C::kChunk, NB = C::kBlocks;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ q4::Ring<kChunk, ST> bars;
 
@@ -132,37 +133,35 @@ __global__ void __launch_bounds__(kThreads, kQ4ScanCtasPerSm) q4_scan_kernel(con
         if (tid == 0) bars.drain(at.st, at.phase);
         return;
       }
-      const int blk = c * kWarps + warp;           // this warp's 32 positions
-      const int rest = pc.L - blk * 32;
-      float x[4][4];
-      if (rest > 0) {
-        const uint8_t *codes = ring + at.st * C::kStage + (warp * 32 + g) * (D / 2);
-        const uint8_t *scales = ring + at.st * C::kStage + C::kCodes + (warp * 32 + g) * (D / 16);
-        float d[4][1][4];
-        q4::score_tiles<D, 1, 4, Q2>(codes, scales, tq, qh, ql, d);
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[nt][e] = d[nt][0][e];
+      const int blk0 = (c * kWarps + warp) * NB;   // this warp's 32-position blocks
+      const int rest0 = pc.L - blk0 * 32;
+      float x[4 * NB][1][4];
+      if (rest0 > 0) {
+        const int row = warp * NB * 32 + g;
+        q4::score_tiles<D, 1, 4 * NB, Q2>(ring + at.st * C::kStage + row * (D / 2),
+                                          ring + at.st * C::kStage + C::kCodes + row * (D / 16), tq, qh, ql, x);
       }
       __syncwarp();
       if (lane == 0) sm100::mbar_arrive(&bars.empty[at.st]);
       at.advance();
-      if (rest <= 0 || !saga_in_bounds(blk < p.nblk, p.err)) continue;
-      if (rest < 32 && MODE != kQ4Dump) {          // positions behind the end: below every score
+      if (rest0 < 32 * NB && MODE != kQ4Dump) {    // positions behind the end: below every score
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int nt = 0; nt < 4 * NB; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (8 * nt + 2 * tq + (e & 1) >= rest) x[nt][e] = MODE == kQ4Step ? __int_as_float(0x7fc00000) : -INFINITY;
+            if (8 * nt + 2 * tq + (e & 1) >= rest0)
+              x[nt][0][e] = MODE == kQ4Step ? __int_as_float(0x7fc00000) : -INFINITY;
       }
 
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int rr = 0; rr < 2 * NB; ++rr) {
+        const int r = rr % 2, blk = blk0 + rr / 2, rest = rest0 - 32 * (rr / 2);
+        if (rest <= 0 || !saga_in_bounds(blk < p.nblk, p.err)) break;
+        const auto score = [&](int nt, int e) { return x[4 * (rr / 2) + nt][0][2 * r + e]; };
         if constexpr (MODE == kQ4Max) {
-          float mx = fmaxf(x[0][2 * r], x[0][2 * r + 1]);
+          float mx = fmaxf(score(0, 0), score(0, 1));
 #pragma unroll
-          for (int nt = 1; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(x[nt][2 * r], x[nt][2 * r + 1]));
+          for (int nt = 1; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(score(nt, 0), score(nt, 1)));
           if (live[r]) (o_max + 8 * r * p.nblk * 4)[blk * 4] = static_cast<uint16_t>(order_key(mx * fac[r]) >> 16);
         } else if constexpr (MODE == kQ4Dump) {
           float *o = o_dump + 8 * r * p.row_stride + static_cast<int64_t>(blk) * 32;
@@ -170,14 +169,14 @@ __global__ void __launch_bounds__(kThreads, kQ4ScanCtasPerSm) q4_scan_kernel(con
           for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              if (live[r] && 8 * nt + 2 * tq + e < rest) o[8 * nt + e] = x[nt][2 * r + e] * fac[r];
+              if (live[r] && 8 * nt + 2 * tq + e < rest) o[8 * nt + e] = score(nt, e) * fac[r];
         } else {
           // NaN behind the end compares false
           float a[8];
           uint32_t mask = 0u;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            a[i] = x[i / 2][2 * r + i % 2] * fac[r];
+            a[i] = score(i / 2, i % 2) * fac[r];
             if (a[i] >= thr[r]) mask |= 1u << (8 * (i / 2) + i % 2);
           }
           mask <<= 2 * tq;
