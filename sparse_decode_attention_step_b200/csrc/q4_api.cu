@@ -58,7 +58,7 @@ Q4Plan q4_plan(const saga_shape &s) {
   Q4Plan p;
   const int64_t items = static_cast<int64_t>(s.B) * s.h_q;
   p.nblk = std::max<int64_t>(1, ceil_div(s.max_l_kv, 32));
-  p.scan = ctas_for(s, q4_scan_chunk(s.d), kQ4ScanCtasPerSm);
+  p.scan = ctas_for(s, kQ4ScanChunk, kQ4ScanCtasPerSm);
   const int64_t sb = std::min(std::max<int64_t>(1, p.nblk / kGatherBlocks),
                               std::max<int64_t>(1, kGatherCtasPerSm * kSms / items));
   p.blk_per_split = ceil_div(p.nblk, sb);
@@ -262,10 +262,9 @@ saga_status saga_q4_refresh_threshold(const saga_shape *shape, const saga_q4_cac
       return cuda_fail(e, "score dump kernel (4-bit)");
   }
   // 1. the largest score of every eight positions, and the N-th largest of those:
-  // a lower bound of the threshold (-inf with N groups or fewer; for rows that the
-  // select holds on chip whole, two launches fewer without it)
+  // a lower bound of the threshold (-inf with N groups or fewer)
   float *bound = nullptr;
-  if (s.max_l_kv > kQ4SelectKeys) {
+  if (s.max_l_kv > kQ4NoBound) {
     bound = reinterpret_cast<float *>(static_cast<char *>(ws) + pl.off_bound);
     if ((e = launch_q4_scan(p, kQ4Max, s.dtype, s.d, st)) != cudaSuccess)
       return cuda_fail(e, "group maximum kernel (4-bit)");

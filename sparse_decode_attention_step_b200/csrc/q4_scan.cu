@@ -17,10 +17,10 @@
 // bits a value, where writing and reading the rows would move 8 bytes a score.
 //
 // As many CTAs as fit on the GPU share the rows (b, key head) in equal runs of
-// chunks of 256 positions, whatever the lengths (see Work). The chunks (codes
+// chunks of 256 or 512 positions, whatever the lengths (see Work). The chunks (codes
 // and scales, two contiguous ranges) come through a ring of shared-memory stages
-// with untiled bulk copies (see Ring); each of eight warps scores its 32
-// positions: mma.sync m16n8k16 with the heads on M and eight keys on N, a
+// with untiled bulk copies (see Ring); each of eight warps scores its one or two
+// blocks of 32 positions: mma.sync m16n8k16 with the heads on M and eight keys on N, a
 // lane converting consecutive codes of one key row into the B operand. A
 // quad of lanes then holds two heads' 32 scores: their masks of kept positions
 // come together in two shuffles, and a kept score goes to its own place in the
@@ -40,20 +40,28 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxDevices = 64;
 
-template <int D>
+template <int D, int MODE, typename T>
 struct QS {
-  static constexpr int kBlocks = D == 64 ? 2 : 1;               // 32-position blocks per warp and chunk
-  static constexpr int kChunk = q4_scan_chunk(D);
-  static_assert(kChunk == kWarps * kBlocks * 32, "a chunk's blocks");
+  // 32-position blocks per warp and chunk: two spread a chunk's fixed work and give
+  // a warp independent MMAs (8 x 128K positions, heads of 64: the step's pass 36 ->
+  // 31 us; four, with one CTA per SM, 38), where the registers of two CTAs per SM
+  // hold them. At d 128 the step gains (8 x 128K: 51.6 -> 49.8 us with its gather),
+  // the other modes and fp32 queries spill (refresh 67 -> 72).
+  static constexpr int kBlocks = D == 64 || (MODE == kQ4Step && sizeof(T) == 2) ? 2 : 1;
+  static constexpr int kChunk = kWarps * kBlocks * 32;
+  static_assert(kChunk >= kQ4ScanChunk, "the plan counts chunks of at least this");
   static constexpr int kCodes = kChunk * D / 2, kScales = kChunk * D / 16;
-  static constexpr int kStage = kCodes + kScales;               // 9 KB (d 64), 18 KB
-  static constexpr int kStages = D == 64 ? 4 : 5;
-  static constexpr int kRing = kStages * kStage;                // 72, 90 KB: two CTAs per SM
+  static constexpr int kStage = kCodes + kScales;               // 18 or 36 KB
+  // A short ring leaves a step room for the gather's CTAs beside its own (6 stages
+  // instead of 4 cost 15 us of 46, 3 instead of 4 gained 1; 8 x 64K, heads of 64);
+  // the maxima at d 128 want a longer one (refresh of 8 x 64K: 49 us with 5, 53 with 4)
+  static constexpr int kStages = kBlocks == 1 ? 5 : (D == 64 ? 3 : 2);
+  static constexpr int kRing = kStages * kStage;
 };
 
 template <int D, int MODE, typename T>
 __global__ void __launch_bounds__(kThreads, kQ4ScanCtasPerSm) q4_scan_kernel(const Q4Params p) {
-  using C = QS<D>;
+  using C = QS<D, MODE, T>;
   constexpr bool Q2 = sizeof(T) == 4;
   constexpr int ST = C::kStages, kChunk = C::kChunk, NB = C::kBlocks;
   extern __shared__ __align__(128) uint8_t ring[];
@@ -479,11 +487,11 @@ cudaError_t launch_scan(const Q4Params &p, cudaStream_t st) {
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if (!attr_set[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(q4_scan_kernel<D, MODE, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             QS<D>::kRing);
+                             QS<D, MODE, T>::kRing);
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  return launch_pdl(q4_scan_kernel<D, MODE, T>, dim3(p.S), dim3(kThreads), QS<D>::kRing, st, p);
+  return launch_pdl(q4_scan_kernel<D, MODE, T>, dim3(p.S), dim3(kThreads), QS<D, MODE, T>::kRing, st, p);
 }
 
 template <int D, typename T>
