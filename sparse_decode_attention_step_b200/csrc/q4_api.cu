@@ -40,9 +40,10 @@ int ctas_for(const saga_shape &s, int64_t chunk, int64_t ctas_per_sm) {
   return static_cast<int>(std::min(chunks, kSms * ctas_per_sm));
 }
 
-// CTAs of the gather in all, and the blocks of a row that each has at least: few
-// enough that a warp has several batches of rows to overlap.
-constexpr int64_t kGatherCtasPerSm = 4;
+// The blocks of a row that a CTA of the gather has at least, so that a warp has
+// several batches of rows to overlap and a row few records to merge (batch 1, 128K,
+// d 128: 15.7 us for the step, 17.0 with 64). As many CTAs as fit at once otherwise: more
+// leave a second wave half empty (d 128, batch 8: 43.5 us, 49.6 with four per SM).
 constexpr int64_t kGatherBlocks = 128;
 
 // Workspace: error and abort words, the records of the dense call or of the
@@ -60,7 +61,7 @@ Q4Plan q4_plan(const saga_shape &s) {
   p.nblk = std::max<int64_t>(1, ceil_div(s.max_l_kv, 32));
   p.scan = ctas_for(s, kQ4ScanChunk, kQ4ScanCtasPerSm);
   const int64_t sb = std::min(std::max<int64_t>(1, p.nblk / kGatherBlocks),
-                              std::max<int64_t>(1, kGatherCtasPerSm * kSms / items));
+                              std::max<int64_t>(1, q4_gather_ctas_per_sm(s.d) * kSms / items));
   p.blk_per_split = ceil_div(p.nblk, sb);
   p.SB = static_cast<int>(ceil_div(p.nblk, p.blk_per_split));
   p.dense = 0;

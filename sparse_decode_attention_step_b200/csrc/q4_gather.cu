@@ -65,7 +65,7 @@ struct Rows {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 4 : 3) q4_gather_kernel(const Q4Gather p) {
+__global__ void __launch_bounds__(kThreads, q4_gather_ctas_per_sm(D)) q4_gather_kernel(const Q4Gather p) {
   constexpr int NM = D / 16;
   __shared__ int list[kWarps][32 * 32 + kBatch];
   __shared__ float s_acc[kWarps][D], s_m[kWarps], s_l[kWarps];

@@ -76,6 +76,7 @@ struct Q4Gather {
   int64_t vc_sb, vc_sh, nblk, cap, max_l_kv;
   int32_t B, h_q, hpv, SB, blk_per_split;
 };
+constexpr int q4_gather_ctas_per_sm(int d) { return d == 64 ? 4 : 3; }   // that fit at once
 cudaError_t launch_q4_gather(const Q4Gather &p, int d, cudaStream_t st);
 
 }  // namespace saga
