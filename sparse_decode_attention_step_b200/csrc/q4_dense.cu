@@ -36,7 +36,7 @@
 //   L8   5 to 8 heads: one tile, a high and a low MMA into the same sums;
 //   L16  9 to 16 heads (one value head): two such tiles.
 //
-// Bound by instruction issue: about 300 per 32 positions of a key head and a value
+// Bound by instruction issue: about 310 per 32 positions of a key head and a value
 // head of 64 (64 conversions, 64 scale products, 32 MMAs, the softmax, the nibbles)
 // at 2.3-2.7 a cycle and SM. 8 x 128K positions of 8 + 8 heads of 64 (604 MB): 144
 // us, 4.2 TB/s; 16 sequences of up to 64K, 1 + 4 heads of 128 (201 MB): 69 us, 2.9

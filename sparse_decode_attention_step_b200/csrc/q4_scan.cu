@@ -26,7 +26,7 @@
 // come together in two shuffles, and a kept score goes to its own place in the
 // 32-position block. The step is deterministic.
 //
-// Bound by instruction issue: about 280 per 32 positions and 16 heads (32
+// Bound by instruction issue: about 260 per 32 positions and 16 heads (32
 // conversions, 32 scale products, 16 MMAs, and per score a product, a compare and
 // a mask bit) at 2.3 a cycle and SM. 8 x 128K positions of 2 heads of 64 (75 MB):
 // step 31 us, max 28 us, 2.4-2.7 TB/s, where a copy would take 12.
