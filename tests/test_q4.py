@@ -12,6 +12,10 @@ most the range R of the row's scores in log2 units plus 15); output sums lose
 2 units of 2^-23 per 16 positions of one warp's share (at most 1/8 of a split
 of 16384) and 64 more in the merges. So with e the sum of those,
 |out - out*| <= 2 e sum_t p_t |v_t|, element by element."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -640,3 +644,119 @@ def test_against_the_16_bit_calls():
     live = torch.isfinite(tau)
     assert torch.equal(live, torch.isfinite(tau4))
     assert (tau - tau4)[live].abs().max() <= 2e-5 * tau[live].abs().max()
+
+
+# ---------------------------------------------------------------------------
+# batches and lengths at the ends of the range
+# ---------------------------------------------------------------------------
+def check_refresh(P, N, rows=None):
+    """A refresh with its step: thresholds, masks and outputs against the call's own score rows."""
+    tau = torch.full((P.B, P.h_q), float("nan"), device="cuda")
+    n = P.shp.max_l_kv
+    got = torch.full((P.B, P.h_q, n), 777.0, device="cuda")
+    cnt = torch.zeros(P.B, P.h_q, dtype=torch.int32, device="cuda")
+    mask = torch.full((P.B, P.h_q, n), 2, dtype=torch.uint8, device="cuda")
+    saga.q4_refresh_threshold(P.shp, P.cache, P.q, P.l, N, tau, P.ws, out=P.out, sel_count=cnt, sel_mask=mask,
+                              scores=got)
+    assert saga.read_device_error(P.ws) == 0
+    r, t = got.cpu().numpy(), tau.cpu().numpy()
+    for b in range(P.B):
+        for j in range(P.h_q):
+            row = r[b, j, :P.lens[b]]
+            want = np.float32(orc.nth_largest_f32(row, N)) if row.size else np.float32(-np.inf)
+            assert want.view(np.uint32) == t[b, j].view(np.uint32), (b, j)
+            if row.size:
+                assert np.max(np.abs(row - P.scores(b, j))) <= P.delta(b, j)
+    check_step(P, P.out, cnt, mask, tau, rows)
+    again = torch.zeros_like(tau)
+    saga.q4_refresh_threshold(P.shp, P.cache, P.q, P.l, N, again, P.ws)
+    assert torch.equal(tau, again)
+
+
+@pytest.mark.parametrize("dtype", [saga.SAGA_BF16, saga.SAGA_F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_refresh_by_a_bound(d, dtype):
+    check_refresh(Problem(5, 8, 2, 4, d, dtype, 8200, [8197, 0, 33, 6500, 512], 51, gscale=True, pad=True), 50)
+
+
+@pytest.mark.parametrize("N", [1, 3000, 40000])
+def test_refresh_longer_than_the_bound_keeps_on_chip(N):
+    check_refresh(Problem(1, 3, 1, 1, 64, saga.SAGA_BF16, 150004, [150001], 52), N, rows=[1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_more_sequences_than_lanes(d):
+    lens = np.random.default_rng(3).integers(0, 900, 70)
+    lens[::3] = 0
+    lens[40:66] = 0
+    lens[69] = 900
+    P = Problem(70, 4, 1, 2, d, saga.SAGA_BF16, 900, lens, 53)
+    saga.q4_dense_decode(P.shp, P.cache, P.q, P.l, P.out, P.ws)
+    P.check_all(P.out)
+    check_refresh(P, 30)
+
+
+def test_rows_of_no_positions():
+    P = Problem(3, 8, 2, 4, 64, saga.SAGA_BF16, 4, [0, 0, 0], 54, max_l=0)
+    tau = torch.zeros(3, 8, device="cuda")
+    saga.q4_refresh_threshold(P.shp, P.cache, P.q, P.l, 5, tau, P.ws)
+    assert torch.all(tau == -np.inf)
+    for call in (lambda: saga.q4_dense_decode(P.shp, P.cache, P.q, P.l, P.out, P.ws),
+                 lambda: saga.q4_decode_step(P.shp, P.cache, P.q, P.l, tau, P.out, P.ws)):
+        P.out.fill_(float("nan"))
+        call()
+        assert torch.all(P.out == 0) and saga.read_device_error(P.ws) == 0
+
+
+# ---------------------------------------------------------------------------
+# the bounds-checked build: the same results, no check fails
+# ---------------------------------------------------------------------------
+CHAIN = r"""
+import sys
+import numpy as np, torch
+import sparse_decode_attention_step_b200 as saga
+saga.load()
+res = {}
+for d, hq, hk, hv in ((64, 16, 2, 4), (128, 12, 1, 4)):
+    gen = torch.Generator("cuda").manual_seed(d)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=gen).bfloat16()
+    shp = saga.shape(3, hq, hk, hv, d, saga.SAGA_BF16, 8200)
+    cache, ws = saga.Q4Cache(shp), saga.Q4Workspace(shp)
+    l = torch.zeros(3, dtype=torch.int32, device="cuda")
+    n = torch.tensor([8190, 0, 301], dtype=torch.int32, device="cuda")
+    saga.q4_append_kv(shp, cache, rand(3, 8190, hk, d), rand(3, 8190, hv, d), 8190, l, ws, n_new=n)
+    saga.q4_append_kv(shp, cache, rand(3, 1, hk, d), rand(3, 1, hv, d), 1, l, ws)
+    K, V = torch.zeros(3, hk, 300, d, device="cuda").bfloat16(), torch.zeros(3, hv, 300, d, device="cuda").bfloat16()
+    saga.q4_read_kv(shp, cache, 300, l, K, V, ws)
+    q = rand(3, hq, d)
+    out, tau = torch.zeros(3, hq, d, device="cuda"), torch.zeros(3, hq, device="cuda")
+    saga.q4_dense_decode(shp, cache, q, l, out, ws)
+    dense = out.cpu().numpy().copy()
+    saga.q4_refresh_threshold(shp, cache, q, l, 60, tau, ws, out=out)
+    fresh = out.cpu().numpy().copy()
+    saga.q4_decode_step(shp, cache, rand(3, hq, d), l, tau, out, ws)
+    for k, x in (("K", K.float()), ("V", V.float()), ("tau", tau), ("step", out), ("l", l)):
+        res[f"d{d}_{k}"] = x.cpu().numpy()
+    res[f"d{d}_dense"], res[f"d{d}_fresh"] = dense, fresh
+    res[f"d{d}_err"] = np.array([saga.read_device_error(ws)])
+np.savez(sys.argv[1], **res)
+"""
+
+
+def test_checked_build_agrees(tmp_path):
+    from sparse_decode_attention_step_b200 import build
+    if not os.path.exists(build.CHECK_LIB_PATH):
+        build.build(check=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    got = []
+    for checked in ("0", "1"):
+        path = str(tmp_path / f"{checked}.npz")
+        env = dict(os.environ, SAGA_CHECKED_BUILD=checked,
+                   PYTHONPATH=root + os.pathsep + os.environ.get("PYTHONPATH", ""))
+        r = subprocess.run([sys.executable, "-c", CHAIN, path], env=env, cwd=root, capture_output=True, text=True,
+                           timeout=300)
+        assert r.returncode == 0, r.stderr[-2000:]
+        got.append(np.load(path))
+    for k in got[0].files:
+        assert np.array_equal(got[0][k], got[1][k]), k
+    assert not got[1]["d64_err"].any() and not got[1]["d128_err"].any()
