@@ -357,11 +357,12 @@ __global__ void __launch_bounds__(kSelThreads, 3) q4_bound_kernel(const BoundPar
 // One CTA per row (b, query head). The listed scores are gathered on chip (in no
 // particular order; they are only counted), then their N-th largest. A sparse
 // list's positions are gathered first, a thread per 32-position block, then all
-// its scores at once; a dense one (a short row, where N groups are most of it)
-// is read a block per warp, where one thread per block would walk up to 32 entries
-// (smallest refresh 28 -> 24 us when it came). Lists too long for the chip (ties at the bound, or a large N) are
-// read that way again for each histogram. 512 rows of up to 128K, N 1024: 19 us, of
-// which listing the positions takes 10 and the histograms 3.
+// its scores at once; a dense one (more than eight a block: a short row, where N
+// groups are most of it) is read a block per warp, which waits for memory at every
+// few blocks where a thread would walk up to 32 entries (8 rows of 32K, N 2048: 41
+// us for the refresh with positions, 69 by blocks; 8 rows of 4096 without a bound:
+// 27 with positions, 22 by blocks). Lists too long for the chip (ties at the
+// bound, or a large N) are read by blocks again for each histogram.
 constexpr int kSelWords = kQ4SelectKeys;        // keys, or half as many keys and positions: 40 KB, four CTAs per SM
 
 struct SelParams {
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(kSelThreads, 4) q4_select_kernel(const SelPara
     if (lane == 0 && c != 0u) atomicAdd(&s_n, c);
     __syncthreads();
     n = s_n;
-    sparse = n <= kSelWords / 2 && n <= 2u * nb;
+    sparse = n <= kSelWords / 2 && n <= 8u * nb;
     const bool on_chip = n <= (sparse ? kSelWords / 2 : kSelWords);
     if (sparse) {
       for (int i0 = 0; i0 < nb; i0 += kSelThreads * U) {
