@@ -760,3 +760,26 @@ def test_checked_build_agrees(tmp_path):
     for k in got[0].files:
         assert np.array_equal(got[0][k], got[1][k]), k
     assert not got[1]["d64_err"].any() and not got[1]["d128_err"].any()
+
+
+@pytest.mark.parametrize("N", [1, 40, 7000])
+def test_nan_and_infinite_queries_in_long_rows(N):
+    """The same where the refresh takes its bound from the group maxima."""
+    P = Problem(2, 16, 2, 4, 64, saga.SAGA_BF16, 8200, [8197, 6500], 29)
+    tau = torch.zeros(2, 16, device="cuda")
+
+    def run():
+        saga.q4_refresh_threshold(P.shp, P.cache, P.q, P.l, N, tau, P.ws, out=P.out)
+        return tau.clone().cpu(), P.out.clone().cpu()
+    clean = run()
+    P.q[0, 1, 3] = float("nan")
+    P.q[0, 9, :] = float("inf")
+    P.q[1, 2, 5] = float("inf")
+    P.q[1, 14, :] = float("nan")
+    got = run()
+    assert saga.read_device_error(P.ws) == 0
+    ok = torch.ones(2, 16, dtype=torch.bool)
+    for b, j in ((0, 1), (0, 9), (1, 2), (1, 14)):
+        ok[b, j] = False
+    for x, y in zip(got, clean):
+        assert torch.equal(x[ok], y[ok])
