@@ -134,7 +134,7 @@ __device__ __forceinline__ void load_q(const uint16_t *row, int tq, float (&v)[D
 // Rows are brought to fp16 by a power of two that puts their largest magnitude
 // into [2^14, 2^15): bf16 queries are then exact down to 2^-24 / 2^15 of the
 // row's maximum, and fp32 queries keep 22 bits in a high and a low half (Q2).
-// `row` < 0 marks a row of zeros. Returns the inverse of the power of two.
+// A row that is not `live` is one of zeros. Returns the inverse of the power of two.
 template <int D, typename T, bool Q2, int HALF>
 __device__ __forceinline__ float q_frag(const T *q, bool live, int tq, uint32_t (&hi)[D / 16][4],
                                         uint32_t (&lo)[Q2 ? D / 16 : 1][4]) {
@@ -166,6 +166,16 @@ __device__ __forceinline__ float q_frag(const T *q, bool live, int tq, uint32_t 
       }
     }
   return __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+}
+
+// What turns a raw score (fp16 operands' units) into a score times `unit`; `inv` is the
+// power of two from q_frag, g the key head's scale. g comes last, so that a large one
+// overflows nothing that a small query row would bring back. The result stays between the
+// smallest and the largest fp32 value: positions behind a row's end are -inf and keys of
+// zeros 0 before they are multiplied, and a factor of 0 or infinity would make them NaN.
+// (A factor under 2^-126 has fewer bits: of scores under 2^-100, which no softmax sees.)
+__device__ __forceinline__ float score_factor(float unit, float inv, float g) {
+  return fminf(fmaxf(unit * kQ4Unit * inv * g, 0x1p-149f), 0x1.fffffep127f);
 }
 
 // Eight codes of two value rows (keys k and k + 1 of an MMA step) into A operands:

@@ -182,7 +182,7 @@ q4_dense_kernel(const Q4Params p) {
     // ---- query rows ----------------------------------------------------------
     uint32_t qh[MT][D / 16][4], ql[Q2 ? MT : 1][Q2 ? D / 16 : 1][4];
     float fac[2 * MT];                               // raw score -> log2 units, per row tile
-    const float unit = p.scale * kLog2e * kQ4Unit * (p.k_g != nullptr ? __ldg(p.k_g + kh) : 1.f);
+    const float unit = p.scale * kLog2e, gk = p.k_g != nullptr ? __ldg(p.k_g + kh) : 1.f;
     const T *qb = static_cast<const T *>(p.q) + b * p.q_sb;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
@@ -191,13 +191,13 @@ q4_dense_kernel(const Q4Params p) {
       const int hd0 = MODE == kRowsS ? (g & 3) : g;
       const int hd1 = MODE == kRowsS ? (g & 3) : (MODE == kRowsL16 ? 8 + g : g);
       const int v0 = MODE == kRowsL16 ? 0 : vg * VPW + r0, v1 = MODE == kRowsL16 ? 0 : vg * VPW + r1;
-      fac[r0] = unit * q4::q_frag<D, T, Q2, 0>(
-                           qb + static_cast<int64_t>(kh * G + v0 * HPV + hd0) * p.q_sh, hd0 < HPV, tq,
-                           qh[mt], ql[Q2 ? mt : 0]);
+      fac[r0] = q4::score_factor(
+          unit, q4::q_frag<D, T, Q2, 0>(qb + static_cast<int64_t>(kh * G + v0 * HPV + hd0) * p.q_sh, hd0 < HPV, tq,
+                                        qh[mt], ql[Q2 ? mt : 0]), gk);
       if constexpr (NRT % 2 == 0) {
-        fac[r1] = unit * q4::q_frag<D, T, Q2, 1>(
-                             qb + static_cast<int64_t>(kh * G + v1 * HPV + hd1) * p.q_sh, hd1 < HPV, tq,
-                             qh[mt], ql[Q2 ? mt : 0]);
+        fac[r1] = q4::score_factor(
+            unit, q4::q_frag<D, T, Q2, 1>(qb + static_cast<int64_t>(kh * G + v1 * HPV + hd1) * p.q_sh, hd1 < HPV, tq,
+                                          qh[mt], ql[Q2 ? mt : 0]), gk);
       } else {
         fac[r1] = 0.f;
 #pragma unroll

@@ -122,10 +122,10 @@ __global__ void __launch_bounds__(kThreads, kQ4ScanCtasPerSm) q4_scan_kernel(con
     __syncwarp();
     uint32_t qh[1][D / 16][4], ql[1][Q2 ? D / 16 : 1][4];
     float fac[2], thr[2];
-    const float unit = p.scale * kQ4Unit * (p.k_g != nullptr ? __ldg(p.k_g + pc.kh) : 1.f);
+    const float gk = p.k_g != nullptr ? __ldg(p.k_g + pc.kh) : 1.f;
     const T *qb = static_cast<const T *>(p.q) + b * p.q_sb + static_cast<int64_t>(j0 + g) * p.q_sh;
-    fac[0] = unit * q4::q_frag<D, T, Q2, 0>(qb, live[0], tq, qh[0], ql[0]);
-    fac[1] = unit * q4::q_frag<D, T, Q2, 1>(qb + 8 * p.q_sh, live[1], tq, qh[0], ql[0]);
+    fac[0] = q4::score_factor(p.scale, q4::q_frag<D, T, Q2, 0>(qb, live[0], tq, qh[0], ql[0]), gk);
+    fac[1] = q4::score_factor(p.scale, q4::q_frag<D, T, Q2, 1>(qb + 8 * p.q_sh, live[1], tq, qh[0], ql[0]), gk);
     if (MODE == kQ4Step) {
 #pragma unroll
       for (int r = 0; r < 2; ++r)
