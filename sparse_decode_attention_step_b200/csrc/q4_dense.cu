@@ -393,7 +393,7 @@ q4_dense_kernel(const Q4Params p) {
 #pragma unroll
     for (int r = 0; r < NRT; ++r) {
       const int v = MODE == kRowsL16 ? 0 : vg * VPW + r;
-      const float gv = kQ4Unit * (p.v_g != nullptr ? __ldg(p.v_g + kh * C::VPG + v) : 1.f);
+      const float gv = p.v_g != nullptr ? __ldg(p.v_g + kh * C::VPG + v) : 1.f;
       if constexpr (MODE == kRowsS) {                // the low halves' sums: rows 4-7
 #pragma unroll
         for (int n = 0; n < NM; ++n)
@@ -407,11 +407,12 @@ q4_dense_kernel(const Q4Params p) {
         const int hd = (MODE == kRowsL16 ? 8 * r : 0) + 2 * tq + e;
         if (hd >= HPV || (MODE == kRowsS && tq >= 2)) continue;
         const int hg = v * HPV + hd;                 // head of the group
-        float f = gv;
+        float f = 1.f, gh = 1.f;                     // the head scale comes last, times values that fit
         float *o;
         if (whole) {
           o = p.out + (static_cast<int64_t>(b) * p.h_q + kh * G + hg) * D;
-          f = gave_up ? __int_as_float(0x7fc00000) : gv / lh;
+          f = gave_up ? __int_as_float(0x7fc00000) : kQ4Unit / lh;
+          gh = gv;
         } else {
           o = p.partials + (static_cast<int64_t>(cta + b * p.h_k + kh) * G + hg) * (D + kRecPad);
           if (g == 0) *reinterpret_cast<float4 *>(o) = make_float4(mh, lh, gave_up ? 1.f : 0.f, 0.f);
@@ -420,7 +421,7 @@ q4_dense_kernel(const Q4Params p) {
 #pragma unroll
         for (int n = 0; n < NM; ++n)
           *reinterpret_cast<float2 *>(o + g * (D / 8) + 2 * n) =
-              make_float2(acc[r][n][e] * f, acc[r][n][2 + e] * f);
+              make_float2(acc[r][n][e] * f * gh, acc[r][n][2 + e] * f * gh);
       }
     }
   }
@@ -494,7 +495,8 @@ __global__ void __launch_bounds__(kCombThreads) q4_combine_kernel(const Q4Params
   for (int w = 1; w < kCombWarps; ++w) l += s_l[w];
 #pragma unroll
   for (int i = 1; i < kPar; ++i) a += s_acc[tid + i * D];
-  p.out[static_cast<int64_t>(blockIdx.x) * D + tid] = m == INFINITY ? __int_as_float(0x7fc00000) : a / l;
+  const float gv = p.v_g != nullptr ? __ldg(p.v_g + j / (p.h_q / p.h_v)) : 1.f;
+  p.out[static_cast<int64_t>(blockIdx.x) * D + tid] = m == INFINITY ? __int_as_float(0x7fc00000) : a / l * kQ4Unit * gv;
 }
 
 template <int D, int VPW, int MODE, int NG, typename T>

@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, q4_gather_ctas_per_sm(D)) q4_gather_
     lt = fmaf(c, s_l[w], lt);
     if (tid < D) at = fmaf(c, s_acc[w][tid], at);
   }
-  const float unit = kQ4Unit * (p.v_g != nullptr ? __ldg(p.v_g + vh) : 1.f);
+  const float gv = p.v_g != nullptr ? __ldg(p.v_g + vh) : 1.f;
   if (p.SB > 1) {
     float *rec = row_rec + sb * kRec;
     if (tid < D) __stcg(rec + kRecPad + tid, at);
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, q4_gather_ctas_per_sm(D)) q4_gather_
   }
   // an empty selection is a zero row; a scan that gave up a NaN one
   if (tid < D) {
-    const float o = lt > 0.f ? at / lt * unit : 0.f;
+    const float o = lt > 0.f ? at / lt * kQ4Unit * gv : 0.f;
     p.out[static_cast<int64_t>(bj) * D + tid] = n_all < 0 ? __int_as_float(0x7fc00000) : o;
   }
   if (tid == 0) {

@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(const Q4Read p) {
   const uint32_t *codes = reinterpret_cast<const uint32_t *>(is_v ? p.vc : p.kc) + first;
   const uint8_t *scales = (is_v ? p.vs : p.ks) + first / 2;      // first is even: rows are
   const float *gp = is_v ? p.v_g : p.k_g;
-  const float g = kQ4Unit * (gp != nullptr ? __ldg(gp + h) : 1.f);
+  const float g = gp != nullptr ? __ldg(gp + h) : 1.f;
   T *out = static_cast<T *>(is_v ? p.V : p.K) + (static_cast<int64_t>(b) * heads + h) * p.n * p.d;
   uint32_t w[U], s[U];
 #pragma unroll
@@ -294,9 +294,10 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(const Q4Read p) {
     float x[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t v = q4::mul_f16x2(c[e], q4::scale_f16(s[u]));
+      // code * scale (at most 2688, so exact in fp16), without the factor 2^-8 of the
+      // scale; then times g, one rounding to fp32
+      const uint32_t v = q4::mul_f16x2(q4::mul_f16x2(c[e], 0x5c005c00u), q4::scale_f16(s[u]));
       const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v));
-      // the stored value is exact before g: one rounding to fp32
       x[2 * e] = f.x * g;
       x[2 * e + 1] = f.y * g;
     }

@@ -81,3 +81,48 @@ def test_zero_keys_times_large_queries(dtype):
     saga.q4_dense_decode(P.shp, P.cache, P.q, P.l, P.out, P.ws)
     P.check_all(P.out)
     check_refresh(P, 7)
+
+
+@pytest.mark.parametrize("g", [2.0 ** 120, 2.0 ** -149])
+@pytest.mark.parametrize("heads,d,cap", [((8, 2, 2), 64, 300), ((8, 2, 2), 64, 8200), ((12, 1, 4), 128, 8200)])
+def test_value_heads_of_any_scale(heads, d, cap, g):
+    """v_g at the ends of the range, in rows of one CTA and in rows that several share."""
+    P = Problem(2, *heads, d, saga.SAGA_BF16, cap, [cap - 3, 0], 65, gscale=True)
+    # blocks of scale 2^-6 for the large g and of 2^8 for the small one: values the type holds
+    P.cache.v_scales.fill_(0x08 if g > 1 else 0x78)
+    P.cache.v_g.fill_(g)
+    P.V = q4.values(P.cache.v_codes.cpu().numpy(), P.cache.v_scales.cpu().numpy(), np.float32(g))
+    tau = torch.full((2, heads[0]), -np.inf, device="cuda")
+    cuda = lambda x: x.double().cpu().numpy()
+    for call in (lambda: saga.q4_dense_decode(P.shp, P.cache, P.q, P.l, P.out, P.ws),
+                 lambda: saga.q4_decode_step(P.shp, P.cache, P.q, P.l, tau, P.out, P.ws)):
+        call()
+        if g > 1:
+            P.check_all(P.out)
+            continue
+        # outputs of few bits: half a step of 2^-149 and the bound's share of the largest value
+        assert not P.out[1].any()
+        for j in range(heads[0]):
+            A = P.scores(0, j)
+            p = np.exp(A - A.max())
+            V = P.V[0, j * heads[2] // heads[0], :cap - 3]
+            want = p @ V / p.sum()
+            assert np.all(np.abs(cuda(P.out)[0, j] - want) <= 2.0 ** -149 + 1e-4 * np.abs(V).max())
+
+
+@pytest.mark.parametrize("dtype", [saga.SAGA_BF16, saga.SAGA_F32])
+@pytest.mark.parametrize("g", [2.0 ** 120, 1.25 * 2.0 ** 120, 2.0 ** -149])
+def test_read_back_of_any_head_scale(g, dtype):
+    P = Problem(2, 8, 2, 4, 64, dtype, 300, [300, 41], 66, gscale=True)
+    for codes, scales in ((P.cache.k_codes, P.cache.k_scales), (P.cache.v_codes, P.cache.v_scales)):
+        codes[:, :, 7:9] = 0
+        scales.fill_(0x08 if g > 1 else 0x78)
+    P.cache.k_g.fill_(g)
+    P.cache.v_g.fill_(g)
+    tt = torch.float32 if dtype == saga.SAGA_F32 else torch.bfloat16
+    K, V = torch.zeros(2, 2, 300, 64, dtype=tt, device="cuda"), torch.zeros(2, 4, 300, 64, dtype=tt, device="cuda")
+    saga.q4_read_kv(P.shp, P.cache, 300, P.l, K, V, P.ws)
+    for got, codes, scales in ((K, P.cache.k_codes, P.cache.k_scales), (V, P.cache.v_codes, P.cache.v_scales)):
+        want = q4.values(codes.cpu().numpy(), scales.cpu().numpy(), np.float32(g)).astype(np.float32)
+        for b, n in enumerate((300, 41)):
+            assert torch.equal(got[b, :, :n].cpu(), torch.from_numpy(want[b, :, :n]).to(tt))
