@@ -21,11 +21,17 @@
 //            operand pairs two keys per register, so the codes of two rows are
 //            interleaved by nibble before they are converted.
 //
-// Probabilities are scaled by 2^7 and split into a high and a low fp16 half
-// (22 bits; fp16 alone would cost the fp32 output its precision). The running
-// maximum follows the scores lazily: a row is rescaled when its maximum has
-// grown by more than 2^8 of weight, so that P stays below 2^15. The tensor cores
-// cut their fp32 sums off instead of rounding them, so a sum runs over a warp's
+// Probabilities are split into a high and a low fp16 half (22 bits; fp16 alone
+// would cost the fp32 output its precision), relative to the largest score of the
+// warp's positions of one chunk and scaled by 2^15, which is as far up as fp16's
+// range goes: a probability loses bits only when it lies more than 2^17 under that
+// maximum, and then at most 2^-38 of it. The chunk's sums are brought to the row's
+// running maximum when they are added to its own, by the factor that the addition
+// takes anyway; the running maximum follows lazily, and a row is rescaled when its
+// maximum has grown by more than 2^8 of weight. (P relative to the running maximum
+// lost the bits of every key far under a dominating one: with keys of value 0 that
+// outweigh the others 2^20 times each, 1.6e-4 of the output.) The tensor cores cut
+// their fp32 sums off instead of rounding them, so a sum runs over a warp's
 // positions of one chunk there and over chunks in rounded fp32 additions.
 //
 // Rows of the score tile (each 8-row tile belongs to one value head):
@@ -55,7 +61,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kPShift = 7.f;                  // P is scaled by 2^kPShift
+constexpr float kPShift = 15.f;                 // P is scaled by 2^kPShift
 constexpr float kLazy = 8.f;                    // log2 growth of a row's maximum that rescales it
 constexpr int kMaxDevices = 64;
 
@@ -77,6 +83,10 @@ struct QD {
   // three stages of the ring room and the accumulators their registers.
   static constexpr int kKeys = D == 64 ? (VPG == 1 ? 128 : 80) : (VPG == 1 ? 64 : VPG == 2 ? 32 : 48);
   static constexpr int NT = kKeys / 8, NJ = kKeys / 16;         // key tiles, 16-key steps
+  // Row tiles of a product of P and V, and the 16-key steps whose values are converted
+  // before it: in mode L16 one or two at a time, whose registers hold the second tile's sums (8 x
+  // 128K, one head of 128: 65 us in bf16 and 77 in fp32; 67 and 80 with all steps at once)
+  static constexpr int NP = MODE == kRowsL16 ? 2 : 1, JB = MODE != kRowsL16 ? NJ : D == 64 ? 2 : 1;
   static constexpr int KC = SL * kKeys;
   static constexpr int kCodes = KC * D / 2, kScales = KC * D / 16;
   static constexpr int kStage = (kCodes + kScales) * (1 + VPG);
@@ -114,6 +124,7 @@ q4_dense_kernel(const Q4Params p) {
   using C = QD<D, VPW, MODE, NG>;
   constexpr bool Q2 = sizeof(T) == 4;
   constexpr int NRT = C::NRT, MT = C::MT, NM = C::NM, ST = C::kStages, KC = C::KC, NT = C::NT, NJ = C::NJ;
+  constexpr int NP = C::NP, JB = C::JB;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ q4::Ring<KC, ST> bars;
 
@@ -249,7 +260,7 @@ q4_dense_kernel(const Q4Params p) {
             }
         }
 
-        // ---- running maxima, followed lazily ----------------------------------
+        // ---- the chunk's maxima; running maxima, followed lazily --------------
         float cand[NRT];
         bool grow = false;
 #pragma unroll
@@ -281,14 +292,17 @@ q4_dense_kernel(const Q4Params p) {
 
         // ---- probabilities, as B operands: keys 16 j + .. of row g -------------
         uint32_t ph[NRT][NJ][2], pl[MODE == kRowsS ? 1 : NRT][NJ][2];
+        float to_row[NRT];                       // from the chunk's maximum to the row's
 #pragma unroll
         for (int r = 0; r < NRT; ++r) {
-          const float bias = m[r] == -INFINITY ? 0.f : kPShift - m[r];
+          const float bias = cand[r] == -INFINITY ? 0.f : kPShift - cand[r];
+          to_row[r] = cand[r] == -INFINITY ? 0.f : q4::ex2(cand[r] - m[r]);
+          float sum = 0.f;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const float p0 = q4::ex2(fmaf(x[r][nt][0], fac[r], bias));
             const float p1 = q4::ex2(fmaf(x[r][nt][1], fac[r], bias));
-            l[r] += p0 + p1;
+            sum += p0 + p1;
             // the high half is p cut off at fp16's 11 bits, the low one the rest
             const float h0 = __uint_as_float(__float_as_uint(p0) & 0xffffe000u);
             const float h1 = __uint_as_float(__float_as_uint(p1) & 0xffffe000u);
@@ -299,6 +313,7 @@ q4_dense_kernel(const Q4Params p) {
               pl[r][nt / 2][nt % 2] = q4::pack_f16(p0 - h0, p1 - h1);
             }
           }
+          l[r] = fmaf(to_row[r], sum, l[r]);
         }
 
         // ---- P V: MMA key k of a 16-key step is row tq (k = 2 tq), tq + 4 (2 tq + 1),
@@ -307,40 +322,58 @@ q4_dense_kernel(const Q4Params p) {
 #pragma unroll
         for (int vw = 0; vw < VPW; ++vw) {
           const int v = vg * VPW + vw;
+          // the factors of the tile's rows 2 tq and 2 tq + 1, ahead of the products (mode L16:
+          // behind them, where they hold no registers meanwhile)
+          float f0, f1;
+          const auto columns = [&](int r) {
+            f0 = __shfl_sync(0xffffffffu, to_row[r], tq * 8);
+            f1 = __shfl_sync(0xffffffffu, to_row[r], tq * 8 + 4);
+          };
+          if (MODE != kRowsL16) columns(vw);
           const uint8_t *vc = codes + (1 + v) * C::kCodes + (row0 + tq) * (D / 2) + g * (D / 16);
           const uint8_t *vs = scales + (1 + v) * C::kScales + (row0 + tq) * (D / 16) + (D == 64 ? g / 2 : g);
 #pragma unroll
           for (int u = 0; u < D / 64; ++u) {         // eight dims at a time
-            uint32_t a[NJ][4][4];
+            float t[NP][4][4];                       // of tile vw (mode L16: of both)
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
+            for (int j0 = 0; j0 < NJ; j0 += JB) {
+              uint32_t a[JB][4][4];
 #pragma unroll
-              for (int pr = 0; pr < 2; ++pr) {
-                const int r0 = 16 * j + 8 * pr, r1 = r0 + 4;
-                const uint32_t wa = *reinterpret_cast<const uint32_t *>(vc + r0 * (D / 2) + 4 * u);
-                const uint32_t wb = *reinterpret_cast<const uint32_t *>(vc + r1 * (D / 2) + 4 * u);
-                q4::value_pair(wa, wb, vs[r0 * (D / 16)], vs[r1 * (D / 16)], pr, a[j]);
-              }
+              for (int j = 0; j < JB; ++j)
 #pragma unroll
-            for (int r = 0; r < NRT; ++r) {
-              if (MODE != kRowsL16 && r != vw) continue;
-              float t[4][4];
-#pragma unroll
-              for (int j = 0; j < NJ; ++j) {
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                  if (j == 0) q4::mma_first(t[n], a[j][n], ph[r][j][0], ph[r][j][1]);
-                  else q4::mma(t[n], a[j][n], ph[r][j][0], ph[r][j][1]);
+                for (int pr = 0; pr < 2; ++pr) {
+                  const int r0 = 16 * (j0 + j) + 8 * pr, r1 = r0 + 4;
+                  const uint32_t wa = *reinterpret_cast<const uint32_t *>(vc + r0 * (D / 2) + 4 * u);
+                  const uint32_t wb = *reinterpret_cast<const uint32_t *>(vc + r1 * (D / 2) + 4 * u);
+                  q4::value_pair(wa, wb, vs[r0 * (D / 16)], vs[r1 * (D / 16)], pr, a[j]);
                 }
-                if constexpr (MODE != kRowsS) {
 #pragma unroll
-                  for (int n = 0; n < 4; ++n) q4::mma(t[n], a[j][n], pl[r][j][0], pl[r][j][1]);
+              for (int i = 0; i < NP; ++i) {
+                const int r = MODE == kRowsL16 ? i : vw;
+#pragma unroll
+                for (int j = 0; j < JB; ++j) {
+                  const int k = j0 + j;
+#pragma unroll
+                  for (int n = 0; n < 4; ++n) {
+                    if (k == 0) q4::mma_first(t[i][n], a[j][n], ph[r][k][0], ph[r][k][1]);
+                    else q4::mma(t[i][n], a[j][n], ph[r][k][0], ph[r][k][1]);
+                  }
+                  if constexpr (MODE != kRowsS) {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) q4::mma(t[i][n], a[j][n], pl[r][k][0], pl[r][k][1]);
+                  }
                 }
               }
+            }
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+              const int r = MODE == kRowsL16 ? i : vw;
+              if (MODE == kRowsL16) columns(r);
 #pragma unroll
               for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[r][4 * u + n][e] += t[n][e];
+                for (int e = 0; e < 4; ++e)
+                  acc[r][4 * u + n][e] = fmaf(e % 2 ? f1 : f0, t[i][n][e], acc[r][4 * u + n][e]);
             }
           }
         }

@@ -34,7 +34,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBatch = 32;                       // kept rows per step of a warp
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kPShift = 7.f;                   // as in the dense kernel
+constexpr float kPShift = 15.f;                  // as in the dense kernel: P is relative to its batch
 constexpr float kLazy = 8.f;
 
 // Loads of what is read once, at random: without a line in L1, which the rows of
@@ -130,7 +130,10 @@ __global__ void __launch_bounds__(kThreads, q4_gather_ctas_per_sm(D)) q4_gather_
 #pragma unroll
       for (int n = 0; n < NM; ++n) { acc[n][0] *= c; acc[n][1] *= c; }
     }
-    const float bias = m == -INFINITY ? 0.f : kPShift - m;
+    // P relative to the batch's own maximum; its sums are brought to the running one
+    const float bias = mx == -INFINITY ? 0.f : kPShift - mx;
+    const float f = mx == -INFINITY ? 0.f : q4::ex2(mx - m);
+    float sum = 0.f;
     uint32_t pb[2][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -138,11 +141,12 @@ __global__ void __launch_bounds__(kThreads, q4_gather_ctas_per_sm(D)) q4_gather_
       for (int pr = 0; pr < 2; ++pr) {
         const float p0 = q4::ex2(fmaf(r.a[j][2 * pr], kLog2e, bias));
         const float p1 = q4::ex2(fmaf(r.a[j][2 * pr + 1], kLog2e, bias));
-        l += p0 + p1;
+        sum += p0 + p1;
         const float h0 = __uint_as_float(__float_as_uint(p0) & 0xffffe000u);
         const float h1 = __uint_as_float(__float_as_uint(p1) & 0xffffe000u);
         pb[j][pr] = g < 2 ? q4::pack_f16_rz(fmaf(lo_col, h0, p0), fmaf(lo_col, h1, p1)) : 0u;
       }
+    l = fmaf(f, sum, l);
 #pragma unroll
     for (int u = 0; u < D / 64; ++u) {
       uint32_t a[2][4][4];
@@ -161,8 +165,9 @@ __global__ void __launch_bounds__(kThreads, q4_gather_ctas_per_sm(D)) q4_gather_
         for (int n = 0; n < 4; ++n) q4::mma(t[n], a[j][n], pb[j][0], pb[j][1]);
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        acc[4 * u + n][0] += t[n][0] + t[n][1];  // lanes with tq == 0 hold columns 0 and 1
-        acc[4 * u + n][1] += t[n][2] + t[n][3];
+        // lanes with tq == 0 hold columns 0 and 1
+        acc[4 * u + n][0] = fmaf(f, t[n][0] + t[n][1], acc[4 * u + n][0]);
+        acc[4 * u + n][1] = fmaf(f, t[n][2] + t[n][3], acc[4 * u + n][1]);
       }
     }
   };

@@ -126,3 +126,87 @@ def test_read_back_of_any_head_scale(g, dtype):
         want = q4.values(codes.cpu().numpy(), scales.cpu().numpy(), np.float32(g)).astype(np.float32)
         for b, n in enumerate((300, 41)):
             assert torch.equal(got[b, :, :n].cpu(), torch.from_numpy(want[b, :, :n]).to(tt))
+
+
+# ---------------------------------------------------------------------------
+# probabilities far under the largest
+# ---------------------------------------------------------------------------
+# Keys of two kinds: "high" ones, of score s and value 0, and "low" ones, of
+# score 0 and value 1, so that out = n w / (m + n w) with w = e^-s, m high and n low
+# keys, in every element. Relative error of out: that of w (the product's factor has
+# four roundings and the product one, each 2^-24 of the exponent s; the exponent's
+# own rounding 2^-20 for an argument under 2^5 in log2 units, 2^-19 in two parts; ex2
+# 2^-22, twice where it is taken in two parts), P's two halves (2^-22), the tensor cores'
+# sums over at most 128 positions (2 units of 2^-23 in each of 16 steps for two
+# halves), 2^-24 of every addition over a warp's chunks, and 2^-21 for the merges and
+# the quotient.
+def rel_bound(s, adds):
+    return 5 * 2.0 ** -24 * s + 2.0 ** -20 + 2.0 ** -19 + 3 * 2.0 ** -22 + 16 * 2.0 ** -22 + 2 * adds * 2.0 ** -24 + 2.0 ** -21
+
+
+def two_kinds(heads, d, B, L, high, weight, dtype):
+    """(shape, cache, q, lengths, workspace, score s, expected output): `high` [L] bool, `weight` of a low key."""
+    h_q, h_k, h_v = heads
+    shp = saga.shape(B, h_q, h_k, h_v, d, dtype, L)
+    g = np.float32(-np.log(weight) * np.sqrt(d) / 4)
+    cache = saga.Q4Cache(shp, k_g=torch.full((h_k,), float(g), device="cuda"))
+    cache.k_scales.fill_(0x38)
+    cache.v_scales.fill_(0x38)
+    cache.k_codes[:, :, high, 0] = 0x06                    # 4, then zeros
+    cache.v_codes[:, :, ~high] = 0x22                      # ones
+    q = torch.zeros(B, h_q, d, device="cuda", dtype=torch.float32 if dtype == saga.SAGA_F32 else torch.bfloat16)
+    q[:, :, 0] = 1
+    s = float(g) * 4 / np.sqrt(d)
+    m, n, w = int(high.sum()), int((~high).sum()), np.exp(-s)
+    l = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    return shp, cache, q, l, saga.Q4Workspace(shp), s, n * w / (m + n * w)
+
+
+# every arrangement of score rows, with the sequences that give each CTA several chunks
+LAYOUTS = [((8, 8, 8), 16), ((8, 1, 1), 64), ((16, 1, 1), 64), ((4, 1, 2), 64), ((16, 1, 2), 64), ((12, 1, 4), 64)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads,B", LAYOUTS)
+@pytest.mark.parametrize("bits", [14, 20, 24])
+def test_dense_keeps_small_weights(bits, heads, B, d):
+    """A few dominating keys at the head of each row, of value 0: what the others carry stays."""
+    L = 16384
+    t = torch.arange(L, device="cuda")
+    shp, cache, q, l, ws, s, want = two_kinds(heads, d, B, L, (t < 1024) & (t % 32 == 0), 1.2345678 * 2.0 ** -bits,
+                                              saga.SAGA_BF16)
+    out = torch.zeros(B, heads[0], d, device="cuda")
+    saga.q4_dense_decode(shp, cache, q, l, out, ws)
+    err = (out.double() / want - 1).abs().max().item()
+    assert err <= rel_bound(s, L // 128), (err, rel_bound(s, L // 128))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bits", [14, 20, 24])
+def test_step_keeps_small_weights(bits, d):
+    """The same for the gather: each of its warps meets dominating keys first, then others."""
+    L, heads, B = 8192, (12, 1, 4), 16
+    t = torch.arange(L, device="cuda")
+    shp, cache, q, l, ws, s, want = two_kinds(heads, d, B, L, t % 256 == 0, 1.2345678 * 2.0 ** -bits, saga.SAGA_BF16)
+    out = torch.zeros(B, heads[0], d, device="cuda")
+    saga.q4_decode_step(shp, cache, q, l, torch.full((B, heads[0]), -np.inf, device="cuda"), out, ws)
+    err = (out.double() / want - 1).abs().max().item()
+    assert err <= rel_bound(s, L // 32), (err, rel_bound(s, L // 32))
+
+
+@pytest.mark.parametrize("dtype", [saga.SAGA_BF16, saga.SAGA_F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads,B", LAYOUTS)
+@pytest.mark.parametrize("bits", [1, 6, 12])
+def test_probabilities_have_their_low_halves(bits, heads, B, d, dtype):
+    """High and low keys in turn: one fp16 half alone would be off by 1.6e-4 here."""
+    L, B = 1024, 2
+    shp, cache, q, l, ws, s, want = two_kinds(heads, d, B, L, torch.arange(L, device="cuda") % 2 == 0,
+                                              1.2345678 * 2.0 ** -bits, dtype)
+    tau = torch.full((B, heads[0]), -np.inf, device="cuda")
+    for call in (lambda o: saga.q4_dense_decode(shp, cache, q, l, o, ws),
+                 lambda o: saga.q4_decode_step(shp, cache, q, l, tau, o, ws)):
+        out = torch.zeros(B, heads[0], d, device="cuda")
+        call(out)
+        err = (out.double() / want - 1).abs().max().item()
+        assert err <= rel_bound(s, L // 32), (err, rel_bound(s, L // 32))
