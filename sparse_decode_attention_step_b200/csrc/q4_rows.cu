@@ -49,10 +49,12 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
 // and a second one from its exact residual rounds it correctly. For t within
 // 2^+-100 and |x| <= 8 t the residuals neither overflow nor lose bits that matter
 // (a quotient small enough for that rounds to code 0 all the same).
+// The residual is taken as q t - x and subtracted: where q is a zero it is +0 (0 t + 0, or -0 +
+// 0), so that -0 - 0 and 0 - 0 leave the quotient its sign.
 __device__ __forceinline__ float quotient(float x, float t, float inv) {
   float q = x * inv;
-  q = fmaf(fmaf(-q, t, x), inv, q);
-  return fmaf(fmaf(-q, t, x), inv, q);
+  q = fmaf(-fmaf(q, t, -x), inv, q);
+  return fmaf(-fmaf(q, t, -x), inv, q);
 }
 
 // A thread's raw block of 16 values, loaded ahead of its conversion.

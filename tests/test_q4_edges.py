@@ -210,3 +210,29 @@ def test_probabilities_have_their_low_halves(bits, heads, B, d, dtype):
         call(out)
         err = (out.double() / want - 1).abs().max().item()
         assert err <= rel_bound(s, L // 32), (err, rel_bound(s, L // 32))
+
+
+# ---------------------------------------------------------------------------
+# negative zeros
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [saga.SAGA_BF16, saga.SAGA_F32])
+@pytest.mark.parametrize("T", [1, 3, 700])
+def test_append_keeps_the_sign_of_zero(T, dtype):
+    """-0 (and a quotient that rounds to it) among other values has the definition's code, 8."""
+    rng = np.random.default_rng(67)
+    shp = saga.shape(2, 4, 2, 4, 64, dtype, 704)
+    x = {k: rng.standard_normal((2, T, h, 64)) for k, h in (("k", 2), ("v", 4))}
+    for a in x.values():
+        r = rng.random(a.shape)
+        a[r < 0.2] = -0.0
+        a[(r >= 0.2) & (r < 0.3)] = 0.0
+        a[(r >= 0.3) & (r < 0.4)] = -1e-38
+    x = {k: stored(a, dtype) for k, a in x.items()}
+    cache, ws = saga.Q4Cache(shp), saga.Q4Workspace(shp)
+    l = torch.zeros(2, dtype=torch.int32, device="cuda")
+    saga.q4_append_kv(shp, cache, dev(x["k"], dtype), dev(x["v"], dtype), T, l, ws)
+    for kind, codes, scales in (("k", cache.k_codes, cache.k_scales), ("v", cache.v_codes, cache.v_scales)):
+        wc, wsc = q4.quantise(x[kind].numpy())
+        assert (wc & 15 == 8).any()
+        assert np.array_equal(codes.cpu().numpy()[:, :, :T], wc.transpose(0, 2, 1, 3))
+        assert np.array_equal(scales.cpu().numpy()[:, :, :T], wsc.transpose(0, 2, 1, 3))
