@@ -132,6 +132,8 @@ saga_status saga_q4_decode_step(const saga_shape *shape, const saga_q4_cache *ca
 /*
  * Refresh over a 4-bit cache: tau[b][j] = the exact N-th largest score of row
  * (b, j), or -inf when N >= l_kv[b], as saga_refresh_threshold; N >= 1.
+ * Where a bounded wait gave up (SAGA_DEVERR_TIMEOUT), tau is NaN in place of a
+ * score, and out and sel_count are as in saga_q4_decode_step then: NaN and -1.
  *   out      nullable: with it, the same call then runs this step's selection
  *            and PV with the fresh tau (out, sel_count and sel_mask as in
  *            saga_q4_decode_step). Without it sel_count and sel_mask must be NULL.

@@ -30,7 +30,8 @@ struct Q4Params {
   float *scores_out;           // dump: [B][h_q][row_stride]
   uint16_t *group_max;         // max: [B * h_q][nblk * 4], largest scores of 8-position groups:
                                // the upper halves of their order keys
-  int32_t *tickets;            // step: [B * h_q + 1] counters of the gather, cleared here
+  int32_t *tickets;            // step: [B * h_q + 1] counters of the gather (the last one of the
+                               // select where no gather follows), cleared here
   uint8_t *sel_mask;           // nullable [B][h_q][row_stride]
   uint32_t *lmask;             // step: [B * h_q][nblk] kept positions of every 32-position block
   float *lscore;               // [B * h_q][nblk * 32] kept scores, each at its position

@@ -52,8 +52,9 @@ constexpr int kQ4ScanCtasPerSm = 2;
 cudaError_t launch_q4_bound(const Q4Params &p, int32_t N, float *bound, cudaStream_t st);
 
 // tau[b][j] = the N-th largest of row (b, j)'s listed scores, all of them at
-// least bound[b][j] (-inf where bound is null), or -inf when N >= l_kv[b]; with `keep`, the lists (and a
-// given sel_mask) are cut down to it.
+// least bound[b][j] (-inf where bound is null), or -inf when N >= l_kv[b]; NaN instead
+// of the former when a score pass of the call gave up. With `keep`, the lists (and a given
+// sel_mask) are cut down to it, and a gather has to follow; without it this ends the call.
 constexpr int kQ4SelectKeys = 10240;   // scores of a row that it holds on chip
 // Rows up to this long go to the select whole: without the maximum pass and the
 // bound a refresh of 4096 positions takes 13.0 us instead of 18.2 (batch 8: 21.7

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, kQ4ScanCtasPerSm) q4_scan_kernel(con
       if (!__all_sync(0xffffffffu, q4::wait_bar(&bars.full[at.st], at.phase, &bars.abort))) {
         if (lane == 0) {
           bars.give_up(p.err);
-          atomicExch(p.abort, 1);                  // the gather poisons this step's records
+          atomicExch(p.abort, 1);                  // the gather, or the select, poisons the call's results
         }
         if (tid == 0) bars.drain(at.st, at.phase);
         return;
@@ -371,6 +371,7 @@ struct SelParams {
   const int32_t *l_kv;
   float *tau;
   uint8_t *sel_mask;             // nullable
+  int32_t *abort, *done;         // the call's abort word, and a counter of its rows (zero)
   int64_t nblk, cap, max_l_kv;
   int32_t h_q, N;
   int32_t keep;                  // cut the masks down to the fresh threshold
@@ -400,6 +401,8 @@ __global__ void __launch_bounds__(kSelThreads, 4) q4_select_kernel(const SelPara
     }
   };
 
+  // a score pass that gave up: its lists may hold anything, and there is no threshold in them
+  const bool gave_up = tid == 0 && *reinterpret_cast<const volatile int32_t *>(p.abort) != 0;
   float tau = -INFINITY;
   bool sparse = false;
   uint32_t n = 0u;
@@ -473,8 +476,16 @@ __global__ void __launch_bounds__(kSelThreads, 4) q4_select_kernel(const SelPara
     // (-0 and +0 compare equal in the scan: the bound's key is the lower one)
     tau = from_order_key(nth_largest(order_key(lo == 0.f ? -0.f : lo), mx, static_cast<uint32_t>(p.N), sh, each));
   }
-  if (tid == 0) p.tau[bj] = tau;
-  if (p.keep == 0) return;
+  if (tid == 0) p.tau[bj] = gave_up && p.N < L ? __int_as_float(0x7fc00000) : tau;
+  if (p.keep == 0) {
+    // no gather follows to end the call: the last row that has read the abort word set
+    // (all rows do, or none) clears it for the next call
+    if (gave_up) {
+      __threadfence();
+      if (atomicAdd(p.done, 1) == static_cast<int32_t>(gridDim.x) - 1) *p.abort = 0;
+    }
+    return;
+  }
   if (p.N < L) {
     const uint32_t k_tau = order_key(tau == 0.f ? -0.f : tau);
     if (sparse) {
@@ -547,7 +558,8 @@ cudaError_t launch_q4_select(const Q4Params &p, int32_t N, const float *bound, f
     if (e != cudaSuccess) return e;
     attr_set[dev].store(true, std::memory_order_release);
   }
-  const SelParams sp{p.lmask, p.lscore, bound, p.l_kv, tau, sel_mask, p.nblk, p.cap, p.max_l_kv, p.h_q, N,
+  const SelParams sp{p.lmask, p.lscore, bound, p.l_kv, tau, sel_mask, p.abort,
+                     p.tickets + p.B * p.h_q, p.nblk, p.cap, p.max_l_kv, p.h_q, N,
                      keep ? 1 : 0};
   return launch_pdl(q4_select_kernel, dim3(p.B * p.h_q), dim3(kSelThreads), kSmem, st, sp);
 }
