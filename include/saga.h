@@ -140,6 +140,8 @@ saga_status saga_decode_step(const saga_shape *shape, const void *q,
 /*
  * Refresh step (Atop-N item 2): tau[b][j] = the exact N-th largest score of
  * row (b, j) under IEEE totalOrder, or -inf when N >= l_kv[b]. N >= 1.
+ * Where a bounded wait gave up (SAGA_DEVERR_TIMEOUT), tau is NaN in place of a
+ * score.
  *   V, out    both NULL: only tau is written. Both non-NULL: the same call
  *             then runs this step's selection and PV with the fresh tau,
  *             exactly as saga_decode_step would (out, sel_count, sel_mask as

@@ -98,12 +98,12 @@ inline Plan make_plan(const saga_shape &s, bool persistent, int64_t ctas_per_sm 
   p.off_lscore = align_up(p.off_lmask + lists * sizeof(uint32_t));
   p.off_scores = align_up(p.off_lscore + lists * 32 * sizeof(float));
   p.off_hist = align_up(p.off_scores + static_cast<size_t>(s.B) * s.h_q * s.max_l_kv * sizeof(float));
-  // the bucket counts and digit-1 histograms follow the top-byte histograms
-  // directly: one memset clears all three
+  // the bucket counts, the digit-1 histograms and the select's counter of rows follow
+  // the top-byte histograms directly: one memset clears all four
   p.gcap = select_list_cap(s.max_l_kv);
   p.off_gcount = p.off_hist + static_cast<size_t>(s.B) * s.h_q * 256 * sizeof(uint32_t);
   p.off_hist1 = p.off_gcount + static_cast<size_t>(s.B) * s.h_q * sizeof(uint32_t);
-  p.off_gcand = align_up(p.off_hist1 + static_cast<size_t>(s.B) * s.h_q * 256 * sizeof(uint32_t));
+  p.off_gcand = align_up(p.off_hist1 + (static_cast<size_t>(s.B) * s.h_q * 256 + 1) * sizeof(uint32_t));
   p.off_tau = align_up(p.off_gcand + static_cast<size_t>(s.B) * s.h_q * p.gcap * sizeof(uint32_t));
   p.off_tie = align_up(p.off_tau + static_cast<size_t>(s.B) * s.h_q * sizeof(float));
   p.total = align_up(p.off_tie + static_cast<size_t>(s.B) * s.h_q * sizeof(int32_t));

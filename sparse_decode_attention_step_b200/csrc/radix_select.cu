@@ -282,7 +282,7 @@ radix_select_kernel(const float *__restrict__ scores, int64_t row_stride,
                     int64_t cap, int64_t max_l_kv, const uint32_t *__restrict__ hist0,
                     int32_t *__restrict__ tie, const uint32_t *__restrict__ gcand,
                     const uint32_t *__restrict__ gcount, const uint32_t *__restrict__ hist1,
-                    int gcap) {
+                    int gcap, int32_t *abort_word, int32_t *done) {
   __shared__ Shared sh;
   extern __shared__ uint32_t cand[];
   pdl_wait();
@@ -290,6 +290,15 @@ radix_select_kernel(const float *__restrict__ scores, int64_t row_stride,
   const int bj = blockIdx.x;
   const int b = bj / h_q;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // A score pass that gave up: there is no threshold in the rows it left. Where the select
+  // ends the call, the last row that has read the abort word set (all rows do, or none)
+  // clears it for the next call.
+  const bool gave_up = tid == 0 && abort_word != nullptr &&
+                       *reinterpret_cast<const volatile int32_t *>(abort_word) != 0;
+  if (gave_up && done != nullptr) {
+    __threadfence();
+    if (atomicAdd(done, 1) == static_cast<int32_t>(gridDim.x) - 1) *abort_word = 0;
+  }
   int64_t L = l_kv[b];
   const int64_t hi = cap < max_l_kv ? cap : max_l_kv;
   if (L < 0) L = 0;
@@ -413,7 +422,7 @@ radix_select_kernel(const float *__restrict__ scores, int64_t row_stride,
     mask |= 0xFFu << shift;
     __syncthreads();
   }
-  if (tid == 0) tau[bj] = from_order_key(prefix);
+  if (tid == 0) tau[bj] = gave_up ? __int_as_float(0x7fc00000) : from_order_key(prefix);
   if (tie == nullptr) return;
 
   // ---- position of the k-th entry equal to tau, in position order -------
@@ -466,8 +475,8 @@ radix_select_kernel(const float *__restrict__ scores, int64_t row_stride,
 cudaError_t launch_radix_select(const float *scores, int64_t row_stride, const int32_t *l_kv,
                                 int N, float *tau, int B, int h_q, int64_t cap, int64_t max_l_kv,
                                 const uint32_t *hist0, int32_t *tie, uint32_t *gcand,
-                                uint32_t *gcount, uint32_t *hist1, int gcap, int sms,
-                                cudaStream_t st) {
+                                uint32_t *gcount, uint32_t *hist1, int gcap, int32_t *abort_word,
+                                int32_t *done, int sms, cudaStream_t st) {
   // the dynamic shared-memory opt-in is per device; set once on each
   static std::atomic<bool> attr_set[kMaxDevices];
   const int smem = kCand * static_cast<int>(sizeof(uint32_t));
@@ -497,7 +506,7 @@ cudaError_t launch_radix_select(const float *scores, int64_t row_stride, const i
   return launch_pdl(radix_select_kernel, dim3(rows), dim3(kThreads), smem, st, scores,
                     row_stride, l_kv, N, tau, h_q, cap, max_l_kv, hist0, tie,
                     two_pass ? gcand : nullptr, two_pass ? gcount : nullptr,
-                    two_pass ? hist1 : nullptr, gcap);
+                    two_pass ? hist1 : nullptr, gcap, abort_word, done);
 }
 
 }  // namespace saga

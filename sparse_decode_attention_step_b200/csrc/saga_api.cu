@@ -122,11 +122,12 @@ saga_status run_dense(const saga_shape &s, const void *q, const void *K, const v
 
 thread_local char g_last_error[256] = "";
 
-// The top-byte histograms the score pass fills, and the bucket counts and
-// digit-1 histograms of the radix select, cleared together (they are
+// The top-byte histograms the score pass fills, and the bucket counts, digit-1
+// histograms and counter of rows of the radix select, cleared together (they are
 // adjacent in the workspace).
 struct SelectBufs {
   uint32_t *hist = nullptr, *gcount = nullptr, *hist1 = nullptr, *gcand = nullptr;
+  int32_t *done = nullptr;
 };
 cudaError_t clear_select_counts(const saga_shape &s, const Plan &pl, void *ws, SelectBufs *b,
                                 cudaStream_t st) {
@@ -136,7 +137,8 @@ cudaError_t clear_select_counts(const saga_shape &s, const Plan &pl, void *ws, S
   b->hist1 = reinterpret_cast<uint32_t *>(wsb + pl.off_hist1);
   b->gcand = reinterpret_cast<uint32_t *>(wsb + pl.off_gcand);
   const size_t rows = static_cast<size_t>(s.B) * s.h_q;
-  return cudaMemsetAsync(b->hist, 0, rows * (256 + 1 + 256) * sizeof(uint32_t), st);
+  b->done = reinterpret_cast<int32_t *>(b->hist1 + rows * 256);
+  return cudaMemsetAsync(b->hist, 0, (rows * (256 + 1 + 256) + 1) * sizeof(uint32_t), st);
 }
 
 }  // namespace
@@ -254,8 +256,8 @@ saga_status saga_refresh_threshold(const saga_shape *shape, const void *q, const
   if (e != cudaSuccess) return cuda_fail(e, "score dump kernel");
   // 2. exact N-th largest per row
   e = launch_radix_select(rows, s.max_l_kv, l_kv, N, tau, s.B, s.h_q, s.cap, s.max_l_kv, hist,
-                          nullptr, sb.gcand, sb.gcount, sb.hist1, pl.gcap, static_cast<int>(kSms),
-                          st);
+                          nullptr, sb.gcand, sb.gcount, sb.hist1, pl.gcap, use_tc(s) ? p.abort : nullptr,
+                          V == nullptr ? sb.done : nullptr, static_cast<int>(kSms), st);
   if (e != cudaSuccess) return cuda_fail(e, "radix select kernel");
   if (V == nullptr) return SAGA_OK;
   // 3. this step's select + PV with the fresh tau, over the very rows tau
@@ -308,8 +310,8 @@ saga_status saga_topn_step(const saga_shape *shape, const void *q, const void *K
   if (e != cudaSuccess) return cuda_fail(e, "score dump kernel");
   // 2. the N-th largest and, when it is tied, the last tied position taken
   e = launch_radix_select(rows, s.max_l_kv, l_kv, N, tau, s.B, s.h_q, s.cap, s.max_l_kv, hist,
-                          tie, sb.gcand, sb.gcount, sb.hist1, pl.gcap, static_cast<int>(kSms),
-                          st);
+                          tie, sb.gcand, sb.gcount, sb.hist1, pl.gcap, nullptr, nullptr,
+                          static_cast<int>(kSms), st);
   if (e != cudaSuccess) return cuda_fail(e, "radix select kernel");
   // 3. the step over exactly those positions, from the stored rows (or, on
   // the tensor-core path when they cannot be streamed, from bit-identical
@@ -376,6 +378,7 @@ saga_status saga_debug_scores(const saga_shape *shape, const void *q, const void
   StepParams p = base_params(s, pl, q, K, nullptr, l_kv, ws);
   p.partials = nullptr;
   p.scores_out = scores;
+  p.abort = nullptr;            // no kernel follows to clear it; the error word tells
   return cuda_check(launch_split(s, p, kModeDump, reinterpret_cast<cudaStream_t>(stream)),
                     "score dump kernel");
 }

@@ -90,3 +90,17 @@ def check(P):
 @pytest.mark.parametrize("cap", [1300, 8200])              # without and with the bound
 def test_q4_refresh(cap):
     check(Four(cap))
+
+
+def test_refresh():
+    check(Sixteen(1300))
+
+
+def test_score_rows_alone_leave_the_word():
+    """The rows that saga_debug_scores writes are no part of a step: it neither reads nor clears the word."""
+    P = Sixteen(1300)
+    P.word.fill_(1)
+    saga.debug_scores(P.shp, P.q, P.K, P.l, torch.zeros(B, H_Q, 1300, device="cuda"), P.ws)
+    assert P.word.item() == 1
+    P.step()
+    assert torch.isnan(P.out).all() and P.word.item() == 0
