@@ -298,24 +298,43 @@ class Q4Cache:
     """The 4-bit caches of one shape: codes [B][h][cap][d/2] and scales
     [B][h][cap][d/16] (uint8) of K and V, and an optional fp32 scale per head
     (k_g [h_k], v_g [h_v]). Arrays not given are allocated through torch, with
-    the shape's strides."""
+    the shape's strides. A given tensor has to be on the GPU that the others are
+    on, of its array's type and size and laid out by the shape's strides; a
+    given address (an int) is taken as it is."""
 
     def __init__(self, shp, k_codes=None, k_scales=None, v_codes=None, v_scales=None, k_g=None,
                  v_g=None, device="cuda"):
-        def given(x, stride_b, stride_h, h, per):
-            if x is not None:
-                return x
-            import torch
-            buf = torch.zeros(shp.B * stride_b // per, dtype=torch.uint8, device=device)
-            return buf.as_strided((shp.B, h, shp.cap, shp.d // per),
-                                  (stride_b // per, stride_h // per, shp.d // per, 1))
-        self.k_codes = given(k_codes, shp.k_stride_b, shp.k_stride_h, shp.h_k, 2)
-        self.k_scales = given(k_scales, shp.k_stride_b, shp.k_stride_h, shp.h_k, 16)
-        self.v_codes = given(v_codes, shp.v_stride_b, shp.v_stride_h, shp.h_v, 2)
-        self.v_scales = given(v_scales, shp.v_stride_b, shp.v_stride_h, shp.h_v, 16)
-        self.k_g, self.v_g = k_g, v_g
+        self.device = None
+
+        def array(name, x, h, per, stride_b, stride_h):
+            size = (shp.B, h, shp.cap, shp.d // per)
+            strides = (stride_b // per, stride_h // per, shp.d // per, 1)
+            if x is None:
+                import torch
+                n = sum((k - 1) * s for k, s in zip(size, strides)) + 1 if shp.cap > 0 else 0
+                x = torch.zeros(n, dtype=torch.uint8, device=device).as_strided(size, strides)
+            return self._given(name, x, "uint8", size, strides)
+        self.k_codes = array("k_codes", k_codes, shp.h_k, 2, shp.k_stride_b, shp.k_stride_h)
+        self.k_scales = array("k_scales", k_scales, shp.h_k, 16, shp.k_stride_b, shp.k_stride_h)
+        self.v_codes = array("v_codes", v_codes, shp.h_v, 2, shp.v_stride_b, shp.v_stride_h)
+        self.v_scales = array("v_scales", v_scales, shp.h_v, 16, shp.v_stride_b, shp.v_stride_h)
+        self.k_g = self._given("k_g", k_g, "float32", (shp.h_k,), (1,))
+        self.v_g = self._given("v_g", v_g, "float32", (shp.h_v,), (1,))
         self.c = saga_q4_cache(_ptr(self.k_codes), _ptr(self.k_scales), _ptr(self.v_codes),
                                _ptr(self.v_scales), _ptr(k_g), _ptr(v_g))
+
+    def _given(self, name, x, dtype, size, strides):
+        if x is None or isinstance(x, int):
+            return x
+        # the stride of a dimension of one entry is never used
+        if (str(x.dtype) != "torch." + dtype or tuple(x.shape) != size or
+                any(n > 1 and a != b for n, a, b in zip(size, x.stride(), strides))):
+            raise SagaError(SAGA_ERR_INVALID_ARG, f"Q4Cache ({name}: {dtype} {list(size)} with strides "
+                            f"{list(strides)} wanted, {x.dtype} {list(x.shape)} with {list(x.stride())} given)")
+        if x.device.type != "cuda" or self.device not in (None, x.device.index):
+            raise SagaError(SAGA_ERR_INVALID_ARG, f"Q4Cache ({name} is not on the GPU of the other arrays)")
+        self.device = x.device.index
+        return x
 
 
 def q4_workspace_size(shp):
@@ -341,8 +360,8 @@ class Q4Workspace:
 
 def _q4(name, shp, cache, ws, stream, *args):
     """Call `name`(shape, cache, args..., workspace, stream). Arguments are ints,
-    None or tensors; a tensor, or the workspace, on another device than the
-    current one is refused (a kernel launched here could not reach it)."""
+    None or tensors; a tensor, the cache or the workspace on another device than
+    the current one is refused (a kernel launched here could not reach it)."""
     import torch
     dev = torch.cuda.current_device()
     if stream is None:
@@ -350,15 +369,17 @@ def _q4(name, shp, cache, ws, stream, *args):
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
     v = []
-    for x in (cache.k_codes, *args):
+    for x in args:
         if isinstance(x, torch.Tensor):
             if x.device.index != dev:
                 raise SagaError(SAGA_ERR_INVALID_ARG, name + " (a tensor that is not on the current device)")
             x = x.data_ptr()
         v.append(x)
+    if cache.device not in (None, dev):
+        raise SagaError(SAGA_ERR_INVALID_ARG, name + " (a cache that is not on the current device)")
     if getattr(ws, "device", dev) != dev:
         raise SagaError(SAGA_ERR_INVALID_ARG, name + " (a workspace that is not on the current device)")
-    rc = getattr(_lib or load(), name)(shp, cache.c, *v[1:], ws.data_ptr(), ws.nbytes, stream)
+    rc = getattr(_lib or load(), name)(shp, cache.c, *v, ws.data_ptr(), ws.nbytes, stream)
     if rc != SAGA_OK:
         raise SagaError(rc, name)
 

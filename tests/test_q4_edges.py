@@ -236,3 +236,29 @@ def test_append_keeps_the_sign_of_zero(T, dtype):
         assert (wc & 15 == 8).any()
         assert np.array_equal(codes.cpu().numpy()[:, :, :T], wc.transpose(0, 2, 1, 3))
         assert np.array_equal(scales.cpu().numpy()[:, :, :T], wsc.transpose(0, 2, 1, 3))
+
+
+# ---------------------------------------------------------------------------
+# other orders of the cache's dimensions
+# ---------------------------------------------------------------------------
+def test_caches_with_the_heads_outermost():
+    """[h][B][cap][d] caches, allocated by Q4Cache and written by append, against the usual order."""
+    got = []
+    for outer in (False, True):
+        gen = torch.Generator("cuda").manual_seed(68)
+        rand = lambda *s: torch.randn(*s, device="cuda", generator=gen).bfloat16()
+        shp = saga.shape(3, 16, 2, 4, 64, saga.SAGA_BF16, 512)
+        if outer:
+            shp.k_stride_b = shp.v_stride_b = 512 * 64
+            shp.k_stride_h = shp.v_stride_h = 3 * 512 * 64
+        cache, ws = saga.Q4Cache(shp), saga.Q4Workspace(shp)
+        l = torch.zeros(3, dtype=torch.int32, device="cuda")
+        n = torch.tensor([512, 0, 77], dtype=torch.int32, device="cuda")
+        saga.q4_append_kv(shp, cache, rand(3, 512, 2, 64), rand(3, 512, 4, 64), 512, l, ws, n_new=n)
+        q, out, tau = rand(3, 16, 64), torch.zeros(3, 16, 64, device="cuda"), torch.zeros(3, 16, device="cuda")
+        saga.q4_dense_decode(shp, cache, q, l, out, ws)
+        dense = out.clone()
+        saga.q4_refresh_threshold(shp, cache, q, l, 20, tau, ws, out=out)
+        assert saga.read_device_error(ws) == 0
+        got.append((cache.k_codes.clone(), cache.v_scales.clone(), dense, out, tau))
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and got[0][2][0].any()
