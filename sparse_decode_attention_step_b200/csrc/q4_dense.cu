@@ -155,6 +155,10 @@ q4_dense_kernel(const Q4Params p) {
     const uint32_t rows = left < KC ? (left + 3) & ~3 : KC;
     const uint32_t nc = rows * (D / 2), ns = rows * (D / 16);
     uint8_t *dst = ring + st * C::kStage, *dsc = dst + (1 + C::VPG) * C::kCodes;
+    if (!saga_in_bounds(b < p.B && kh < p.h_k && left > 0 && t + rows <= p.cap && st < ST, p.err)) {
+      sm100::mbar_arrive(&bars.full[st]);
+      return;
+    }
     sm100::mbar_arrive_expect_tx(&bars.full[st], (nc + ns) * (1 + C::VPG));
     q4::bulk_load(dst, p.kc + kb + t * (D / 2), nc, &bars.full[st]);
     q4::bulk_load(dsc, p.ks + kb / 8 + t * (D / 16), ns, &bars.full[st]);
@@ -447,6 +451,7 @@ q4_dense_kernel(const Q4Params p) {
           f = gave_up ? __int_as_float(0x7fc00000) : kQ4Unit / lh;
           gh = gv;
         } else {
+          if (!saga_in_bounds(cta < p.S && hg < G, p.err)) continue;      // q4_plan: S + B h_k records of G
           o = p.partials + (static_cast<int64_t>(cta + b * p.h_k + kh) * G + hg) * (D + kRecPad);
           if (g == 0) *reinterpret_cast<float4 *>(o) = make_float4(mh, lh, gave_up ? 1.f : 0.f, 0.f);
           o += kRecPad;
@@ -488,7 +493,7 @@ __global__ void __launch_bounds__(kCombThreads) q4_combine_kernel(const Q4Params
   if (nb == 0) return;
   const int64_t x = start + static_cast<int64_t>(kh) * nb;
   const int i0 = work.cta_of(x), n = work.cta_of(x + nb - 1) - i0 + 1;
-  if (n == 1) return;                                // written by its one CTA
+  if (n == 1 || !saga_in_bounds(i0 >= 0 && n > 0 && i0 + n <= p.S, p.err)) return;   // written by its one CTA
 
   // a CTA's record of the next row follows G (D + kRecPad) floats on, and so does
   // the next CTA's of this row

@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, q4_gather_ctas_per_sm(D)) q4_gather_
         }
         for (int e = have + incl - cn; mk != 0u; mk &= mk - 1u, ++e) {
           const int pos = (wb + lane) * 32 + __ffs(mk) - 1;
+          if (!saga_in_bounds(e < 32 * 32 + kBatch, p.err)) break;
           mine[e] = saga_in_bounds(pos < L, p.err) ? pos : 0;
         }
         const int total = __shfl_sync(0xffffffffu, incl, 31);

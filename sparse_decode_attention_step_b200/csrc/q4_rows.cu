@@ -169,6 +169,8 @@ struct AppendHead {
   const T *src;
   uint8_t *codes, *scales;
   int64_t src_row, first;      // elements between the head's new rows; first block of row l_kv[b]
+  int64_t room, given;         // blocks of the head from there on; blocks of its new rows
+  int32_t *err;
   float g;
   int bpr;                     // blocks per row
 
@@ -181,6 +183,9 @@ struct AppendHead {
     codes = is_v ? p.vc : p.kc;
     scales = is_v ? p.vs : p.ks;
     first = (is_v ? b * p.vb_sb + h * p.vb_sh : b * p.kb_sb + h * p.kb_sh) + at * bpr;
+    room = (p.cap - at) * bpr;
+    given = static_cast<int64_t>(p.T) * bpr;
+    err = p.err;
     const float *gp = is_v ? p.v_g : p.k_g;
     g = gp != nullptr ? __ldg(gp + h) : 1.f;
   }
@@ -188,6 +193,7 @@ struct AppendHead {
   __device__ __forceinline__ const T *from(int64_t i) const {
     return src + (i >> (bpr == 4 ? 2 : 3)) * src_row + (i & (bpr - 1)) * 16;
   }
+  __device__ __forceinline__ bool has(int64_t i) const { return saga_in_bounds(i >= 0 && i < given && i < room, err); }
   __device__ __forceinline__ void put(int64_t i, const Raw16 &raw) const {
     quantise_block<T>(raw, g, reinterpret_cast<uint2 *>(codes) + first + i, scales + first + i);
   }
@@ -205,6 +211,7 @@ __global__ void __launch_bounds__(kThreads) q4_append_small_kernel(const Q4Appen
   for (int i = threadIdx.x; i < per_head * (p.h_k + p.h_v); i += kThreads) {
     const AppendHead<T> h(p, b, i / per_head, at);
     Raw16 raw;
+    if (!h.has(i % per_head)) continue;
     load_raw(h.from(i % per_head), raw);
     h.put(i % per_head, raw);
   }
@@ -228,10 +235,10 @@ __global__ void __launch_bounds__(kThreads) q4_append_kernel(const Q4Append p) {
   Raw16 raw[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (i0 + u * kThreads < n) load_raw(h.from(i0 + u * kThreads), raw[u]);
+    if (i0 + u * kThreads < n && h.has(i0 + u * kThreads)) load_raw(h.from(i0 + u * kThreads), raw[u]);
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (i0 + u * kThreads < n) h.put(i0 + u * kThreads, raw[u]);
+    if (i0 + u * kThreads < n && h.has(i0 + u * kThreads)) h.put(i0 + u * kThreads, raw[u]);
 }
 
 __global__ void q4_grow_kernel(const Q4Append p) {
@@ -285,12 +292,16 @@ __global__ void __launch_bounds__(kThreads) q4_read_kernel(const Q4Read p) {
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t i = i0 + u * kThreads;
-    if (i < n) { w[u] = __ldg(codes + i); s[u] = __ldg(scales + i / 2); }
+    // inside of the window and of the head
+    if (i < n && saga_in_bounds(i < p.n * ppr && t0 * ppr + i < p.cap * ppr, p.err)) {
+      w[u] = __ldg(codes + i);
+      s[u] = __ldg(scales + i / 2);
+    }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int64_t i = i0 + u * kThreads;
-    if (i >= n) break;
+    if (i >= n || !saga_in_bounds(i < p.n * ppr && t0 * ppr + i < p.cap * ppr, p.err)) break;
     uint32_t c[4];
     q4::codes_f16(w[u], c);
     float x[8];

@@ -97,6 +97,10 @@ __global__ void __launch_bounds__(kThreads, kQ4ScanCtasPerSm) q4_scan_kernel(con
     const uint32_t rows = left < kChunk ? (left + 3) & ~3 : kChunk;
     const uint32_t nc = rows * (D / 2), ns = rows * (D / 16);
     uint8_t *dst = ring + st * C::kStage;
+    if (!saga_in_bounds(b < p.B && kh < p.h_k && left > 0 && t + rows <= p.cap && st < ST, p.err)) {
+      sm100::mbar_arrive(&bars.full[st]);
+      return;
+    }
     sm100::mbar_arrive_expect_tx(&bars.full[st], nc + ns);
     const uint8_t *codes = p.kc + kb + t * (D / 2), *scales = p.ks + kb / 8 + t * (D / 16);
     if (MODE == kQ4Step) {     // a step's K stream leaves its lists in L2 (8 x 128K: 68.6 -> 67 us)
@@ -372,6 +376,7 @@ struct SelParams {
   float *tau;
   uint8_t *sel_mask;             // nullable
   int32_t *abort, *done;         // the call's abort word, and a counter of its rows (zero)
+  int32_t *err;
   int64_t nblk, cap, max_l_kv;
   int32_t h_q, N;
   int32_t keep;                  // cut the masks down to the fresh threshold
@@ -448,18 +453,19 @@ __global__ void __launch_bounds__(kSelThreads, 4) q4_select_kernel(const SelPara
         at = __shfl_sync(0xffffffffu, at, 31) + incl - mine;
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          for (uint32_t x = m[u]; x != 0u; x &= x - 1u, ++at)
+          for (uint32_t x = m[u]; x != 0u && saga_in_bounds(at < kSelWords / 2, p.err); x &= x - 1u, ++at)
             where[at] = (i0 + u * kSelThreads + tid) * 32 + __ffs(x) - 1;
       }
       __syncthreads();
 #pragma unroll 4
-      for (uint32_t i = tid; i < n; i += kSelThreads) keys[i] = order_key(score[where[i]]);
+      for (uint32_t i = tid; i < n; i += kSelThreads)
+        if (saga_in_bounds(where[i] < nb * 32u, p.err)) keys[i] = order_key(score[where[i]]);
     } else if (on_chip) {
       walk([&](int, uint32_t x, float a) {
         uint32_t at = 0u;
         if (lane == 0 && x != 0u) at = atomicAdd(&s_at, static_cast<uint32_t>(__popc(x)));
         at = __shfl_sync(0xffffffffu, at, 0) + __popc(x & ((1u << lane) - 1u));
-        if ((x >> lane) & 1u) keys[at] = order_key(a);
+        if ((x >> lane) & 1u && saga_in_bounds(at < kSelWords, p.err)) keys[at] = order_key(a);
       });
       __syncthreads();
     }
@@ -559,7 +565,7 @@ cudaError_t launch_q4_select(const Q4Params &p, int32_t N, const float *bound, f
     attr_set[dev].store(true, std::memory_order_release);
   }
   const SelParams sp{p.lmask, p.lscore, bound, p.l_kv, tau, sel_mask, p.abort,
-                     p.tickets + p.B * p.h_q, p.nblk, p.cap, p.max_l_kv, p.h_q, N,
+                     p.tickets + p.B * p.h_q, p.err, p.nblk, p.cap, p.max_l_kv, p.h_q, N,
                      keep ? 1 : 0};
   return launch_pdl(q4_select_kernel, dim3(p.B * p.h_q), dim3(kSelThreads), kSmem, st, sp);
 }

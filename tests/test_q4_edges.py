@@ -1,5 +1,10 @@
 """The 4-bit cache at the ends of its range: head scales and queries of any
-magnitude, probabilities far under the largest, negative zeros."""
+magnitude, probabilities far under the largest, negative zeros, other orders of the
+cache's dimensions, and the bounds-checked build."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -262,3 +267,75 @@ def test_caches_with_the_heads_outermost():
         assert saga.read_device_error(ws) == 0
         got.append((cache.k_codes.clone(), cache.v_scales.clone(), dense, out, tau))
     assert all(torch.equal(a, b) for a, b in zip(*got)) and got[0][2][0].any()
+
+
+# ---------------------------------------------------------------------------
+# the bounds-checked build over every kernel variant: the same bits, no check fails
+# ---------------------------------------------------------------------------
+CHAIN = r"""
+import sys
+import numpy as np, torch
+import sparse_decode_attention_step_b200 as saga
+saga.load()
+res = {}
+# every arrangement of score rows; rows of one position, of partial blocks and chunks, and
+# too long for the select's chip; ties; windows that begin and end inside a row
+for n, (d, heads, cap, lens, N, dt) in enumerate((
+        (64, (8, 8, 8), 9000, (8997, 0, 1, 6401), 50, 1), (128, (8, 1, 1), 1300, (1, 1299, 33, 257), 1300, 1),
+        (64, (16, 1, 1), 40000, (40000, 31, 32, 6145), 9000, 0), (128, (16, 1, 1), 9000, (8191, 2, 9000, 64), 3000, 0),
+        (64, (4, 1, 2), 2000, (2000, 1024, 1, 0), 7, 1), (128, (16, 1, 2), 2000, (1999, 3, 640, 641), 300, 0),
+        (64, (32, 2, 8), 150000, (149999, 0, 7, 512), 2048, 1), (128, (12, 1, 4), 9000, (9000, 5, 192, 193), 1, 1))):
+    B, tt = len(lens), torch.bfloat16 if dt else torch.float32
+    gen = torch.Generator("cuda").manual_seed(n)
+    rand = lambda *s: torch.randn(*s, device="cuda", generator=gen).to(tt)
+    shp = saga.shape(B, *heads, d, saga.SAGA_BF16 if dt else saga.SAGA_F32, cap)
+    cache, ws = saga.Q4Cache(shp), saga.Q4Workspace(shp)
+    l = torch.zeros(B, dtype=torch.int32, device="cuda")
+    T = max(lens) - 1
+    first = torch.tensor([max(x - 1, 0) for x in lens], dtype=torch.int32, device="cuda")
+    saga.q4_append_kv(shp, cache, rand(B, T, heads[1], d), rand(B, T, heads[2], d), T, l, ws, n_new=first)
+    last = torch.tensor([min(x, 1) for x in lens], dtype=torch.int32, device="cuda")
+    saga.q4_append_kv(shp, cache, rand(B, 1, heads[1], d), rand(B, 1, heads[2], d), 1, l, ws, n_new=last)
+    assert l.tolist() == list(lens)
+    cache.k_codes[0, :, 100:600] = cache.k_codes[0, :, :1]       # ties
+    cache.k_scales[0, :, 100:600] = cache.k_scales[0, :, :1]
+    K = torch.zeros(B, heads[1], 301, d, device="cuda", dtype=tt)
+    V = torch.zeros(B, heads[2], 301, d, device="cuda", dtype=tt)
+    saga.q4_read_kv(shp, cache, 301, l, K, V, ws, start=(l - 200).clamp(min=0))
+    q, out = rand(B, heads[0], d), torch.zeros(B, heads[0], d, device="cuda")
+    tau, cnt = torch.zeros(B, heads[0], device="cuda"), torch.zeros(B, heads[0], dtype=torch.int32, device="cuda")
+    mask = torch.zeros(B, heads[0], cap, dtype=torch.uint8, device="cuda")
+    rows = torch.zeros(B, heads[0], cap, device="cuda")
+    for k, call in enumerate((
+            lambda: saga.q4_dense_decode(shp, cache, q, l, out, ws),
+            lambda: saga.q4_refresh_threshold(shp, cache, q, l, N, tau, ws, out=out, sel_count=cnt, sel_mask=mask,
+                                              scores=rows),
+            lambda: saga.q4_refresh_threshold(shp, cache, q, l, max(1, N // 3), tau, ws),
+            lambda: saga.q4_decode_step(shp, cache, q, l, tau, out, ws, sel_count=cnt, sel_mask=mask))):
+        call()
+        for name, x in (("out", out), ("tau", tau), ("cnt", cnt), ("mask", mask), ("rows", rows)):
+            res[f"{n} {k} {name}"] = np.array([int(x.contiguous().view(torch.uint8).to(torch.int64).sum()),
+                                               hash(x.cpu().numpy().tobytes())])
+    res[f"{n} K"], res[f"{n} V"] = K.float().cpu().numpy(), V.float().cpu().numpy()
+    res[f"{n} err"] = np.array([saga.read_device_error(ws)])
+np.savez(sys.argv[1], **res)
+"""
+
+
+def test_checked_build_agrees_in_every_variant(tmp_path):
+    from sparse_decode_attention_step_b200 import build
+    if not os.path.exists(build.CHECK_LIB_PATH):
+        build.build(check=True)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    got = []
+    for checked in ("0", "1"):
+        path = str(tmp_path / f"{checked}.npz")
+        env = dict(os.environ, SAGA_CHECKED_BUILD=checked, PYTHONHASHSEED="0",
+                   PYTHONPATH=root + os.pathsep + os.environ.get("PYTHONPATH", ""))
+        r = subprocess.run([sys.executable, "-c", CHAIN, path], env=env, cwd=root, capture_output=True, text=True,
+                           timeout=300)
+        assert r.returncode == 0, r.stderr[-2000:]
+        got.append(np.load(path))
+    for k in got[0].files:
+        assert np.array_equal(got[0][k], got[1][k]), k
+        assert not k.endswith("err") or not got[1][k].any(), k
