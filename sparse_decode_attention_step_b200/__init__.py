@@ -11,9 +11,11 @@ import ctypes
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
-# SAGA_CHECKED_BUILD=1 selects the bounds-checked build (build.py --check)
+# SAGA_CHECKED_BUILD=1 selects the bounds-checked build (build.py --check),
+# SAGA_SHORT_WAITS_BUILD=1 the one whose 4-bit kernels give up their waits at once (--short-waits)
 LIB_PATH = os.path.join(_HERE, "_lib", "libsaga_b200_check.so"
-                        if os.environ.get("SAGA_CHECKED_BUILD") == "1" else "libsaga_b200.so")
+                        if os.environ.get("SAGA_CHECKED_BUILD") == "1" else "libsaga_b200_short.so"
+                        if os.environ.get("SAGA_SHORT_WAITS_BUILD") == "1" else "libsaga_b200.so")
 
 SAGA_OK = 0
 SAGA_ERR_INVALID_ARG = 1

@@ -279,8 +279,13 @@ __device__ __forceinline__ void bulk_load_once(void *dst, const void *src, uint3
       : "memory");
 }
 
-// Bounded wait of every lane of a warp, given up early when *abort is set.
+// Bounded wait of every lane of a warp, given up early when *abort is set. The short-wait
+// build (-DSAGA_SHORT_WAITS) gives up at once where there is anything to wait for, which
+// runs what follows a give-up: the poisoned results, and the wait for copies in flight.
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const int *abort) {
+#ifdef SAGA_SHORT_WAITS
+  return sm100::mbar_test_wait(bar, parity);
+#else
   if (sm100::mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = sm100::global_ns();
   for (;;) {
@@ -288,6 +293,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const i
     if (*reinterpret_cast<const volatile int *>(abort) != 0) return false;
     if (sm100::global_ns() - t0 > sm100::kWaitLimitNs) return false;
   }
+#endif
 }
 
 // A sequence's length in [0, min(cap, max_l_kv)]; a violation is recorded where

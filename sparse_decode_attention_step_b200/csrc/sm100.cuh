@@ -9,7 +9,11 @@
 namespace saga {
 namespace sm100 {
 
+#ifdef SAGA_SHORT_WAITS
+constexpr uint64_t kWaitLimitNs = 200000000ull;
+#else
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // a wait gives up after 2 s
+#endif
 constexpr uint32_t kSuspendHintNs = 20000;          // sleep per poll while the phase is open
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
