@@ -23,16 +23,18 @@
 //
 // Probabilities are split into a high and a low fp16 half (22 bits; fp16 alone
 // would cost the fp32 output its precision), relative to the largest score of the
-// warp's positions of one chunk and scaled by 2^15, which is as far up as fp16's
-// range goes: a probability loses bits only when it lies more than 2^17 under that
-// maximum, and then at most 2^-38 of it. The chunk's sums are brought to the row's
-// running maximum when they are added to its own, by the factor that the addition
-// takes anyway; the running maximum follows lazily, and a row is rescaled when its
-// maximum has grown by more than 2^8 of weight. (P relative to the running maximum
-// lost the bits of every key far under a dominating one: with keys of value 0 that
-// outweigh the others 2^20 times each, 1.6e-4 of the output.) The tensor cores cut
-// their fp32 sums off instead of rounding them, so a sum runs over a warp's
-// positions of one chunk there and over chunks in rounded fp32 additions.
+// warp's positions of one chunk and scaled by 2^7: a probability loses bits when it
+// lies more than 2^9 under that maximum, and then at most 2^-30 of it. (2^15, as far
+// up as fp16 goes, would move that to 2^-38, but the exponents' arguments would reach
+// 15 instead of 7, and their rounding took the error of ordinary rows from 2.2e-7 to
+// 3.4e-7 of the norm.) The chunk's sums are brought to the row's running maximum when
+// they are added to its own, by the factor that the addition takes anyway; the running
+// maximum follows lazily, and a row is rescaled when its maximum has grown by more than
+// 2^8 of weight. (P relative to the running maximum lost the bits of every key far
+// under a dominating one: with keys of value 0 that outweigh the others 2^20 times
+// each, 1.6e-4 of the output.) The tensor cores cut their fp32 sums off instead of
+// rounding them, so a sum runs over a warp's positions of one chunk there and over
+// chunks in rounded fp32 additions.
 //
 // Rows of the score tile (each 8-row tile belongs to one value head):
 //   S    at most 4 query heads per value head: rows 0-3 the heads, rows 4-7 the
@@ -61,7 +63,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kPShift = 15.f;                 // P is scaled by 2^kPShift
+constexpr float kPShift = 7.f;                  // P is scaled by 2^kPShift
 constexpr float kLazy = 8.f;                    // log2 growth of a row's maximum that rescales it
 constexpr int kMaxDevices = 64;
 

@@ -34,7 +34,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBatch = 32;                       // kept rows per step of a warp
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kPShift = 15.f;                  // as in the dense kernel: P is relative to its batch
+constexpr float kPShift = 7.f;                   // as in the dense kernel: P is relative to its batch
 constexpr float kLazy = 8.f;
 
 // Loads of what is read once, at random: without a line in L1, which the rows of
