@@ -174,7 +174,8 @@ __device__ __forceinline__ float q_frag(const T *q, bool live, int tq, uint32_t 
 // overflows nothing that a small query row would bring back. The result stays between the
 // smallest and the largest fp32 value: positions behind a row's end are -inf and keys of
 // zeros 0 before they are multiplied, and a factor of 0 or infinity would make them NaN.
-// (A factor under 2^-126 has fewer bits: of scores under 2^-100, which no softmax sees.)
+// (A factor under 2^-126 has fewer bits: of scores under 2^-100, which no softmax sees. One
+// that the largest value bounds belongs to scores past 2^120, or of 0.)
 __device__ __forceinline__ float score_factor(float unit, float inv, float g) {
   return fminf(fmaxf(unit * kQ4Unit * inv * g, 0x1p-149f), 0x1.fffffep127f);
 }

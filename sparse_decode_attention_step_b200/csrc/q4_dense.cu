@@ -47,8 +47,9 @@
 // Bound by instruction issue: about 310 per 32 positions of a key head and a value
 // head of 64 (64 conversions, 64 scale products, 32 MMAs, the softmax, the nibbles)
 // at 2.3-2.7 a cycle and SM. 8 x 128K positions of 8 + 8 heads of 64 (604 MB): 144
-// us, 4.2 TB/s; 16 sequences of up to 64K, 1 + 4 heads of 128 (201 MB): 69 us, 2.9
-// TB/s, where four value heads share each key row's scores.
+// us, 4.2 TB/s; 16 sequences of up to 64K, 1 + 4 heads of 128 (201 MB): 70 us, 2.9
+// TB/s, where four value heads share each key row's scores. The factors of the chunks
+// cost 0.4% of the instructions in the first case, and up to 4% of the time at d 128.
 #include <atomic>
 
 #include "kernels.h"
@@ -82,7 +83,9 @@ struct QD {
   // long runs of positions spread a chunk's fixed work (waits, the running maximum,
   // addresses: a hundred instructions): 8 x 128K positions of 8 + 8 heads of 64 took
   // 161 us with 32 at a time, 147 with 48 and 142 with 128. As many as leave two or
-  // three stages of the ring room and the accumulators their registers.
+  // three stages of the ring room and the accumulators their registers: none spill but
+  // at d 128 mode L16 (24 bytes a thread, fp32 queries 188) and fp32 queries of two and
+  // four value heads (28 to 36).
   static constexpr int kKeys = D == 64 ? (VPG == 1 ? 128 : 80) : (VPG == 1 ? 64 : VPG == 2 ? 32 : 48);
   static constexpr int NT = kKeys / 8, NJ = kKeys / 16;         // key tiles, 16-key steps
   // Row tiles of a product of P and V, and the 16-key steps whose values are converted

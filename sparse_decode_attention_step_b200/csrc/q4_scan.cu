@@ -50,8 +50,10 @@ struct QS {
   // 32-position blocks per warp and chunk: two spread a chunk's fixed work and give
   // a warp independent MMAs (8 x 128K positions, heads of 64: the step's pass 36 ->
   // 31 us; four, with one CTA per SM, 38), where the registers of two CTAs per SM
-  // hold them. At d 128 the step gains (8 x 128K: 51.6 -> 49.8 us with its gather),
-  // the other modes and fp32 queries spill (refresh 67 -> 72).
+  // hold them. At d 128 the step gains (8 x 128K: 51.6 -> 49.8 us with its gather)
+  // although it spills 24 bytes a thread; the other modes and fp32 queries would spill so
+  // much that they lose (refresh 67 -> 72), and with one block fp32 queries still spill 12
+  // bytes in the step and 80 in the maxima.
   static constexpr int kBlocks = D == 64 || (MODE == kQ4Step && sizeof(T) == 2) ? 2 : 1;
   static constexpr int kChunk = kWarps * kBlocks * 32;
   static_assert(kChunk >= kQ4ScanChunk, "the plan counts chunks of at least this");
@@ -292,7 +294,8 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t x, uint32_t *s) {
 // ---- the lower bound from the group maxima ---------------------------------------
 // One CTA per row, the maxima's 16-bit keys in registers (those behind the first
 // 128K positions are read again for each histogram). 512 rows of up to 128K: 10 us,
-// the latency of one read and two histograms; four CTAs per SM spill and gain nothing.
+// the latency of one read and two histograms; three CTAs per SM spill 48 bytes a thread,
+// four spill more and gain nothing.
 // Cutting an order key off rounds the score down,
 // so the bound stays one. A row whose rank lies in the eight octaves (1024
 // keys) under its maximum takes one histogram.
